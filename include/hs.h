@@ -226,7 +226,13 @@ hs_status hs_decode_sparse_noalloc(const hs_params* p, const void* q, const void
                                    const int32_t* idx, const int32_t* idx_count, void* o,
                                    float* lse, void* stream);
 
-enum { HS_WS_FULL = 0, HS_WS_SPARSE = 1, HS_WS_DECODE_FULL = 2, HS_WS_DECODE_SPARSE = 3 };
+enum {
+    HS_WS_FULL = 0,
+    HS_WS_SPARSE = 1,
+    HS_WS_DECODE_FULL = 2,
+    HS_WS_DECODE_SPARSE = 3,
+    HS_WS_DECODE_FULL_QUANT = 4 /* hs_decode_step_quant(HS_DECODE_FULL_INDEX) */
+};
 
 /* Bytes of workspace the matching entry point needs for these parameters
  * (0 when none).  Returns (size_t)-1 for invalid parameters. */
@@ -288,6 +294,87 @@ hs_status hs_decode_step_paged(const hs_params* p, const hs_pages* pages, int32_
                                const int32_t* seq_len, int32_t* idx, int32_t* idx_count,
                                void* o, float* lse, float* sel_scores, void* workspace,
                                size_t ws_bytes, void* stream);
+
+/*
+ * Quantised K^F/V^F.  The pages count their KV caches in FP8 ("HySparse
+ * 混合稀疏注意力（一）", the KV-cache table); these entry points hold the cache in
+ * 8-bit or 4-bit codes and attend to the codes directly.
+ *
+ * A row of head_dim values is stored as head_dim codes and one entry of two
+ * bf16 numbers {scale, zero}; a code c stands for scale * c + zero.
+ *   HS_KV_INT4  codes 0..15, head_dim / 2 bytes: element 2j in the low, 2j + 1
+ *               in the high nibble of byte j.  Written as scale =
+ *               bf16((max - min) / 15), zero = bf16(min), c =
+ *               clamp(rint((x - zero) / scale), 0, 15);
+ *   HS_KV_FP8   e4m3 codes, head_dim bytes.  Written as scale =
+ *               bf16(max|x| / 448), zero = 0, c = e4m3(x / scale).
+ * A row whose scale is 0 (constant in 4 bits, zero in 8) has codes 0.  A row
+ * with a NaN or an infinity, or whose scale or zero overflows bf16, gets NaN
+ * for both and reads back as NaN.  The attention takes any codes and entries
+ * (a zero point in HS_KV_FP8 too).
+ *
+ * Arrays (device, 16-byte aligned, dense):
+ *   k_codes, v_codes   [batch][hkv][t_kv][code bytes]
+ *   k_scale, v_scale   [batch][hkv][t_kv][2] bf16
+ * or, with `pages` (NULL: contiguous), pools [n_pages][hkv][page_size][..] with
+ * the rules of hs_sparse_attn_reuse_paged (p->t_kv = max_pages * page_size).
+ * Groups of up to 16 heads, head_dim 64 or 128; queries and outputs bf16.
+ */
+typedef enum { HS_KV_INT4 = 0, HS_KV_FP8 = 1 } hs_kv_format;
+
+typedef struct {
+    int32_t format; /* hs_kv_format */
+    void* k_codes;
+    void* k_scale;
+    void* v_codes;
+    void* v_scale;
+} hs_kv_quant;
+
+/*
+ * Quantises new rows into the cache.  k, v: [batch][hkv][t_q][head_dim] of
+ * p->dtype (bf16 or fp32).  Row j < n_new[b] of sequence b goes to position
+ * seq_len[b] - n_new[b] + j: seq_len is each sequence's length with the new
+ * rows in it, so a decode step passes the seq_len of its attention call.
+ * Rows j >= n_new[b] are padding, and nothing else in the cache is touched.
+ * seq_len, n_new: DEVICE int32 [batch]; NULL: p->q_offset + t_q, and t_q, for
+ * every sequence.  A sequence with n_new outside 0..t_q or seq_len outside
+ * n_new..t_kv, or a row on a bad page, is skipped and sets HS_ERR_BOUNDS.
+ * Only batch, hq, hkv, head_dim, t_q, t_kv, q_offset and dtype of p are used.
+ */
+hs_status hs_kv_quant_write(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                            const void* k, const void* v, const int32_t* seq_len,
+                            const int32_t* n_new, void* stream);
+
+/*
+ * Reads the same rows back: k, v [batch][hkv][t_q][head_dim] of p->dtype get
+ * scale * c + zero, computed in fp32 and rounded once.  Rows j >= n_new[b] and
+ * those of skipped sequences are left as they were.
+ */
+hs_status hs_kv_quant_read(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                           void* k, void* v, const int32_t* seq_len, const int32_t* n_new,
+                           void* stream);
+
+/*
+ * The global branch of hs_sparse_attn_reuse over a quantised cache (token or
+ * block mode, any page size; same index sets, results and errors).
+ */
+hs_status hs_sparse_attn_reuse_quant(const hs_params* p, const hs_kv_quant* kv,
+                                     const hs_pages* pages, const void* q_sparse,
+                                     const int32_t* idx, const int32_t* idx_count,
+                                     void* o_global, float* lse_global, void* stream);
+
+/*
+ * hs_decode_step over a quantised cache: both kinds, same arguments, rules and
+ * results.  HS_DECODE_FULL_INDEX needs lse and a workspace of
+ * hs_workspace_size(p, HS_WS_DECODE_FULL_QUANT) bytes (else HS_ERR_WORKSPACE);
+ * calls that may overlap on the GPU need a workspace each.  HS_DECODE_SPARSE
+ * needs none.  A sequence length outside 1..t_kv gives o = 0, lse = -inf, no
+ * selected keys, and HS_ERR_BOUNDS.
+ */
+hs_status hs_decode_step_quant(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                               int32_t kind, const void* q, const int32_t* seq_len, int32_t* idx,
+                               int32_t* idx_count, void* o, float* lse, float* sel_scores,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /* Failure-detection diagnostic (the pages have no counterpart).  Every wait
  * of a kernel on another role of its CTA (a TMA copy, an MMA, a stage of the

@@ -23,6 +23,9 @@
 #include "sparse.cu"
 #include "decode_simt.cu"
 #include "gate_sink.cu"
+#include "kv_quant.cu"
+#include "sparse_quant.cu"
+#include "decode_quant.cu"
 
 namespace hs {
 static std::atomic<uint64_t> g_launches{0};
@@ -207,9 +210,12 @@ hs_status hs_sparse_attn_reuse(const hs_params* p, const void* q_sparse, const v
 
 size_t hs_workspace_size(const hs_params* p, int32_t which) {
     KParams kp;
-    const bool decode = which == HS_WS_DECODE_FULL || which == HS_WS_DECODE_SPARSE;
-    if (which < HS_WS_FULL || which > HS_WS_DECODE_SPARSE) return (size_t)-1;
+    const bool decode = which == HS_WS_DECODE_FULL || which == HS_WS_DECODE_SPARSE ||
+                        which == HS_WS_DECODE_FULL_QUANT;
+    if (which < HS_WS_FULL || which > HS_WS_DECODE_FULL_QUANT) return (size_t)-1;
     if (resolve(p, decode, &kp) != HS_OK) return (size_t)-1;
+    if (which == HS_WS_DECODE_FULL_QUANT)
+        return mma_shape(kp) && kp.mode == HS_SEL_TOKEN ? hs::decode_quant_workspace(kp) : 0;
     if (decode && !mma_shape(kp))  // wide groups / d = 256: the split-k CUDA-core steps
         return hs::decode_simt_split_supported(kp)
                    ? hs::decode_simt_workspace(kp, which == HS_WS_DECODE_FULL)
@@ -297,6 +303,42 @@ hs_status set_pages(const hs_params* p, const hs_pages* pages, KParams* kp) {
     kp->n_pages = pages->n_pages;
     return HS_OK;
 }
+
+// Checks a quantised cache and its parameters.
+hs_status resolve_quant(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                        bool decode, KParams* kp, hs::QuantCache* c) {
+    hs_status s = resolve(p, decode, kp);
+    if (s != HS_OK) return s;
+    if (!kv) return HS_ERR_INVALID_ARG;
+    if (kv->format != HS_KV_INT4 && kv->format != HS_KV_FP8) return HS_ERR_INVALID_ARG;
+    if (pages && (s = set_pages(p, pages, kp)) != HS_OK) return s;
+    if (!ok_ptr(kv->k_codes) || !ok_ptr(kv->k_scale) || !ok_ptr(kv->v_codes) ||
+        !ok_ptr(kv->v_scale))
+        return HS_ERR_INVALID_ARG;
+    if (!mma_shape(*kp)) return HS_ERR_UNSUPPORTED;
+    // tasks of a launch are counted in 31 bits
+    if ((double)kp->batch * kp->hq * kp->t_q >= 2147483648.0) return HS_ERR_INVALID_ARG;
+    *c = hs::QuantCache{(const uint8_t*)kv->k_codes, (const uint32_t*)kv->k_scale,
+                        (const uint8_t*)kv->v_codes, (const uint32_t*)kv->v_scale};
+    return HS_OK;
+}
+
+hs_status quant_rows(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages, void* k,
+                     void* v, const int32_t* seq_len, const int32_t* n_new, bool write,
+                     void* stream) {
+    KParams kp;
+    hs::QuantCache c;
+    hs_status s = resolve_quant(p, kv, pages, false, &kp, &c);
+    if (s != HS_OK) return s;
+    if (!ok_ptr(k) || !ok_ptr(v) || !ok_opt(seq_len) || !ok_opt(n_new)) return HS_ERR_INVALID_ARG;
+    if (!hs::kv_quant_supported(kp)) return HS_ERR_INVALID_ARG;
+    if (kp.t_q == 0) return HS_OK;
+    return launched(1, [&] {
+        return hs::launch_kv_quant(kp, p->dtype, kv->format, kv->k_codes, kv->k_scale,
+                                   kv->v_codes, kv->v_scale, k, v, seq_len, n_new, write,
+                                   static_cast<cudaStream_t>(stream));
+    });
+}
 }  // namespace
 
 extern "C" {
@@ -350,6 +392,66 @@ hs_status hs_decode_step_paged(const hs_params* p, const hs_pages* pages, int32_
     return launched(1, [&] {
         return hs::launch_decode_sparse(kp, q, k_pool, v_pool, seq_len, idx, idx_count, o, lse,
                                         nullptr, st);
+    });
+}
+
+hs_status hs_kv_quant_write(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                            const void* k, const void* v, const int32_t* seq_len,
+                            const int32_t* n_new, void* stream) {
+    return quant_rows(p, kv, pages, const_cast<void*>(k), const_cast<void*>(v), seq_len, n_new,
+                      true, stream);
+}
+
+hs_status hs_kv_quant_read(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                           void* k, void* v, const int32_t* seq_len, const int32_t* n_new,
+                           void* stream) {
+    return quant_rows(p, kv, pages, k, v, seq_len, n_new, false, stream);
+}
+
+hs_status hs_sparse_attn_reuse_quant(const hs_params* p, const hs_kv_quant* kv,
+                                     const hs_pages* pages, const void* q_sparse,
+                                     const int32_t* idx, const int32_t* idx_count,
+                                     void* o_global, float* lse_global, void* stream) {
+    KParams kp;
+    hs::QuantCache c;
+    hs_status s = resolve_quant(p, kv, pages, false, &kp, &c);
+    if (s != HS_OK) return s;
+    if (!ok_ptr(q_sparse) || !ok_ptr(idx) || !ok_ptr(idx_count) || !ok_ptr(o_global) ||
+        !ok_ptr(lse_global))
+        return HS_ERR_INVALID_ARG;
+    if (p->dtype != HS_BF16) return HS_ERR_UNSUPPORTED;
+    if (kp.t_q == 0) return HS_OK;
+    return launched(1, [&] {
+        return hs::launch_sparse_quant(kp, kv->format, c, q_sparse, idx, idx_count, o_global,
+                                       lse_global, static_cast<cudaStream_t>(stream));
+    });
+}
+
+hs_status hs_decode_step_quant(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
+                               int32_t kind, const void* q, const int32_t* seq_len, int32_t* idx,
+                               int32_t* idx_count, void* o, float* lse, float* sel_scores,
+                               void* workspace, size_t ws_bytes, void* stream) {
+    KParams kp;
+    hs::QuantCache c;
+    hs_status s = resolve_quant(p, kv, pages, true, &kp, &c);
+    if (s != HS_OK) return s;
+    if (kind != HS_DECODE_FULL_INDEX && kind != HS_DECODE_SPARSE) return HS_ERR_INVALID_ARG;
+    if (p->dtype != HS_BF16 || p->mode != HS_SEL_TOKEN) return HS_ERR_UNSUPPORTED;
+    if (!ok_ptr(q) || !ok_ptr(seq_len) || !ok_ptr(idx) || !ok_ptr(idx_count) || !ok_ptr(o) ||
+        !ok_opt(lse) || !ok_opt(sel_scores))
+        return HS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (kind == HS_DECODE_SPARSE)
+        return launched(1, [&] {
+            return hs::launch_decode_sparse_quant(kp, kv->format, c, q, seq_len, idx, idx_count, o,
+                                                  lse, st);
+        });
+    if (!lse) return HS_ERR_INVALID_ARG;
+    if (workspace == nullptr || ws_bytes < hs::decode_quant_workspace(kp) || !aligned16(workspace))
+        return HS_ERR_WORKSPACE;
+    return launched(hs::decode_quant_kernel_count(kp, sel_scores != nullptr), [&] {
+        return hs::launch_decode_quant(kp, kv->format, c, q, seq_len, idx, idx_count, o, lse,
+                                       sel_scores, workspace, st);
     });
 }
 

@@ -119,6 +119,26 @@ cudaError_t launch_token_select_wide(const KParams& p, const void* q, const void
                                      const float* lse, int32_t* idx, int32_t* cnt, float* sel,
                                      void* ws, size_t ws_bytes, cudaStream_t st);
 
+// Quantised K^F/V^F (format: hs_kv_format; d = 64 or 128, groups of up to 16
+// heads): rows written and read back, and the attention steps over them.
+struct QuantCache;
+bool kv_quant_supported(const KParams& p);
+cudaError_t launch_kv_quant(const KParams& p, int dtype, int format, void* k_codes, void* k_entry,
+                            void* v_codes, void* v_entry, void* k, void* v,
+                            const int32_t* seq_len, const int32_t* n_new, bool write,
+                            cudaStream_t st);
+cudaError_t launch_sparse_quant(const KParams& p, int format, const QuantCache& c, const void* q,
+                                const int32_t* idx, const int32_t* cnt, void* o, float* lse,
+                                cudaStream_t st);
+cudaError_t launch_decode_sparse_quant(const KParams& p, int format, const QuantCache& c,
+                                       const void* q, const int32_t* seq_len, const int32_t* idx,
+                                       const int32_t* cnt, void* o, float* lse, cudaStream_t st);
+size_t decode_quant_workspace(const KParams& p);
+int decode_quant_kernel_count(const KParams& p, bool sel);
+cudaError_t launch_decode_quant(const KParams& p, int format, const QuantCache& c, const void* q,
+                                const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,
+                                float* lse, float* sel, void* ws, cudaStream_t st);
+
 // Sparse decode step with its scratch in a file-scope device array.
 size_t noalloc_scratch_bytes();
 cudaError_t launch_decode_sparse_noalloc(const KParams& p, const void* q, const void* kc,

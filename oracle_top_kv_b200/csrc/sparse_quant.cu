@@ -1,0 +1,214 @@
+// sparse_quant.cu -- the sparse layers over a quantised K^F/V^F: attention of
+// a layer's own query over the rows of an index set, read as codes
+// (quant_kv.cuh).  Prefill: one warp per (query row, KV group).  Decode: one
+// thread-block cluster per (sequence, KV group); the unit's rows are dealt to
+// its warps in steps, partials are merged per CTA in shared memory and over
+// the cluster in distributed shared memory.
+#include <atomic>
+
+#include "hs_common.cuh"
+#include "hs_kernels.cuh"
+#include "quant_kv.cuh"
+
+namespace hs {
+namespace sq {
+
+constexpr int kWarps = 4;
+// Keys of a step: 32 4-bit rows or 16 8-bit ones fill the same registers.
+template <int F> constexpr int kStep = F == HS_KV_INT4 ? 32 : 16;
+
+// Writes a unit's heads from a warp's finished accumulators.
+template <int D, class A>
+__device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o, float* lse,
+                                           size_t head0, size_t stride) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        const int h = gid + 8 * hr;
+        if (h >= g) continue;
+        const float inv = st.l[hr] == 0.f ? 0.f : 1.f / st.l[hr];
+        const size_t row = head0 + h * stride;
+        __nv_bfloat16* dst = o + row * D + t * (D / 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = pack_bf16(st.o[j + 2 * i][2 * hr + e] * inv,
+                                     st.o[j + 2 * i + 1][2 * hr + e] * inv);
+                *reinterpret_cast<uint4*>(dst + e * (D / 8) + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        if (t == 0) lse[row] = st.l[hr] == 0.f ? -INFINITY : (st.m[hr] + log2f(st.l[hr])) * kLn2;
+    }
+}
+
+template <int D, int F>
+__global__ void __launch_bounds__(kWarps * 32)
+    sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
+                        const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
+                        __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+    const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (task >= (long long)p.batch * p.hkv * p.t_q) return;
+    const int j = (int)(task % p.t_q);
+    const int unit = (int)(task / p.t_q);
+    const int u = unit % p.hkv, b = unit / p.hkv;
+    const size_t head0 = ((size_t)b * p.hq + (size_t)u * p.group) * p.t_q + j;
+    QAttend<D, F, kStep<F>> st;
+    st.init(q + head0 * D, (size_t)p.t_q * D, p.group);
+    const int n = clamp_count(cnt[task], p.ksel) * p.block_size;
+    const QIndex src{idx + (size_t)task * p.ksel, n,           p.block_size,
+                     p.q_offset + j,              p.bt != nullptr, page_map(p, b, u)};
+    const int steps = (n + kStep<F> - 1) / kStep<F>;
+    st.run(unit_cache<D, F>(p, cache, unit), src, 0, 1, steps, p.scale_log2);
+    st.finish();
+    store_rows<D>(st, p.group, o, lse, head0, (size_t)p.t_q);
+}
+
+// Weight of a partial with reference m under the common reference M.
+__device__ __forceinline__ float merge_weight(float m, float M) {
+    return m == -INFINITY ? 0.f : exp2f(m - M);
+}
+
+template <int D, int F>
+__global__ void __launch_bounds__(kWarps * 32)
+    decode_sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
+                               const int32_t* __restrict__ seq_len,
+                               const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
+                               int csize, __nv_bfloat16* __restrict__ o,
+                               float* __restrict__ lse) {
+    using A = QAttend<D, F, kStep<F>>;
+    extern __shared__ __align__(16) float smem[];  // kWarps + 1 partials
+    const int warp = threadIdx.x >> 5, g = p.group;
+    const int crank = csize > 1 ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / csize;
+    const int u = unit % p.hkv, b = unit / p.hkv;
+    const int L = seq_len[b];
+    const bool valid = L >= 1 && L <= p.t_kv;
+    const size_t head0 = (size_t)b * p.hq + (size_t)u * g;
+    A st;
+    st.init(q + head0 * D, D, g);
+    if (valid) {
+        const int n = clamp_count(cnt[unit], p.ksel);
+        const QIndex src{idx + (size_t)unit * p.ksel, n, 1, L - 1, p.bt != nullptr,
+                         page_map(p, b, u)};
+        st.run(unit_cache<D, F>(p, cache, unit), src, crank * kWarps + warp, kWarps * csize,
+               (n + kStep<F> - 1) / kStep<F>, p.scale_log2);
+    } else if (crank == 0 && threadIdx.x == 0) {
+        set_status(HS_ERR_BOUNDS);
+    }
+    st.finish();
+    st.store_part(smem + warp * A::kPart, g);
+    __syncthreads();
+    // the CTA's partial
+    float* mine = smem + kWarps * A::kPart;
+    for (int e = threadIdx.x; e < g * D; e += blockDim.x) {
+        const int h = e / D;
+        float M = -INFINITY, l = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * A::kPart + 2 * h]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = merge_weight(smem[w * A::kPart + 2 * h], M);
+            l += smem[w * A::kPart + 2 * h + 1] * f;
+            acc += smem[w * A::kPart + 32 + e] * f;
+        }
+        mine[32 + e] = acc;
+        if (e % D == 0) {
+            mine[2 * h] = M;
+            mine[2 * h + 1] = l;
+        }
+    }
+    if (csize > 1) cluster_sync_all();
+    else __syncthreads();
+    // each CTA of the cluster writes a share of the heads
+    const uint32_t at = smem_u32(mine);
+    auto rd = [&](int r, int off) -> float {
+        return csize > 1 ? ld_cluster_f32(at + 4u * off, (uint32_t)r) : mine[off];
+    };
+    for (int e = crank * blockDim.x + threadIdx.x; e < g * D; e += csize * blockDim.x) {
+        const int h = e / D;
+        float M = -INFINITY, l = 0.f, acc = 0.f;
+        for (int r = 0; r < csize; ++r) M = fmaxf(M, rd(r, 2 * h));
+        for (int r = 0; r < csize; ++r) {
+            const float f = merge_weight(rd(r, 2 * h), M);
+            l += rd(r, 2 * h + 1) * f;
+            acc += rd(r, 32 + e) * f;
+        }
+        o[(head0 + h) * D + e % D] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+        if (e % D == 0 && lse) lse[head0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+    if (csize > 1) cluster_sync_all();  // peers keep their shared memory until all have read
+}
+
+template <int D, int F>
+static cudaError_t launch_sparse_t(const KParams& p, const QuantCache& c, const void* q,
+                                   const int32_t* idx, const int32_t* cnt, void* o, float* lse,
+                                   cudaStream_t st) {
+    const long long tasks = (long long)p.batch * p.hkv * p.t_q;
+    sparse_quant_kernel<D, F><<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
+        p, c, (const __nv_bfloat16*)q, idx, cnt, (__nv_bfloat16*)o, lse);
+    return cudaGetLastError();
+}
+
+template <int D, int F>
+static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const void* q,
+                                   const int32_t* seq_len, const int32_t* idx, const int32_t* cnt,
+                                   void* o, float* lse, cudaStream_t st) {
+    auto kern = decode_sparse_quant_kernel<D, F>;
+    const size_t smem = (kWarps + 1) * QAttend<D, F, kStep<F>>::kPart * sizeof(float);
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 148;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    // Widest cluster (a portable size) whose CTAs still run in one wave, two
+    // to an SM, with a step for every warp.
+    const int units = p.batch * p.hkv;
+    const int steps = (p.ksel + kStep<F> - 1) / kStep<F>;
+    int csize = 1;
+    while (csize < 8 && units * csize * 2 <= 2 * sms && kWarps * csize < steps) csize *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(units * csize));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, c, (const __nv_bfloat16*)q, seq_len, idx, cnt, csize,
+                              (__nv_bfloat16*)o, lse);
+}
+
+}  // namespace sq
+
+cudaError_t launch_sparse_quant(const KParams& p, int format, const QuantCache& c, const void* q,
+                                const int32_t* idx, const int32_t* cnt, void* o, float* lse,
+                                cudaStream_t st) {
+    if (format == HS_KV_INT4)
+        return p.head_dim == 64 ? sq::launch_sparse_t<64, HS_KV_INT4>(p, c, q, idx, cnt, o, lse, st)
+                                : sq::launch_sparse_t<128, HS_KV_INT4>(p, c, q, idx, cnt, o, lse, st);
+    return p.head_dim == 64 ? sq::launch_sparse_t<64, HS_KV_FP8>(p, c, q, idx, cnt, o, lse, st)
+                            : sq::launch_sparse_t<128, HS_KV_FP8>(p, c, q, idx, cnt, o, lse, st);
+}
+
+cudaError_t launch_decode_sparse_quant(const KParams& p, int format, const QuantCache& c,
+                                       const void* q, const int32_t* seq_len, const int32_t* idx,
+                                       const int32_t* cnt, void* o, float* lse, cudaStream_t st) {
+    if (format == HS_KV_INT4)
+        return p.head_dim == 64
+                   ? sq::launch_decode_t<64, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, st)
+                   : sq::launch_decode_t<128, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, st);
+    return p.head_dim == 64
+               ? sq::launch_decode_t<64, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, st)
+               : sq::launch_decode_t<128, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, st);
+}
+
+}  // namespace hs

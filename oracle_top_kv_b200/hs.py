@@ -23,11 +23,14 @@ HS_BF16, HS_FP32 = 0, 1
 HS_SEL_BLOCK, HS_SEL_TOKEN = 0, 1
 HS_DECODE_FULL_INDEX, HS_DECODE_SPARSE = 0, 1
 HS_WS_FULL, HS_WS_SPARSE, HS_WS_DECODE_FULL, HS_WS_DECODE_SPARSE = 0, 1, 2, 3
+HS_WS_DECODE_FULL_QUANT = 4
+HS_KV_INT4, HS_KV_FP8 = 0, 1
 
 EXPORTS = ("hs_full_attn_index", "hs_sparse_attn_reuse", "hs_decode_step", "hs_workspace_size",
            "hs_device_status", "hs_status_string", "hs_launch_count", "hs_decode_sparse_noalloc",
            "hs_set_wait_limit", "hs_sparse_attn_reuse_paged", "hs_decode_step_paged",
-           "hs_set_select_sampling")
+           "hs_set_select_sampling", "hs_kv_quant_write", "hs_kv_quant_read",
+           "hs_sparse_attn_reuse_quant", "hs_decode_step_quant")
 
 
 class HsError(RuntimeError):
@@ -56,6 +59,18 @@ class hs_pages(ctypes.Structure):
 def make_pages(block_table, page_size, n_pages) -> hs_pages:
     """hs_pages for a [batch][max_pages] int32 device block table."""
     return hs_pages(_ptr(block_table), int(page_size), int(block_table.shape[-1]), int(n_pages))
+
+
+class hs_kv_quant(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("k_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+def make_kv_quant(fmt, k_codes, k_scale, v_codes, v_scale) -> hs_kv_quant:
+    """hs_kv_quant over uint8 code and bf16 {scale, zero} tensors; fmt "int4" or "fp8"."""
+    return hs_kv_quant({"int4": HS_KV_INT4, "fp8": HS_KV_FP8}[fmt], _ptr(k_codes), _ptr(k_scale),
+                       _ptr(v_codes), _ptr(v_scale))
 
 
 def make_params(batch, hq, hkv, head_dim, t_q, t_kv, q_offset=0, dtype="bf16", mode="block",
@@ -93,6 +108,11 @@ def load(path: str = LIB_PATH):
     PG = ctypes.POINTER(hs_pages)
     lib.hs_sparse_attn_reuse_paged.argtypes = [PP, PG, P, P, P, P, P, P, P, P]
     lib.hs_decode_step_paged.argtypes = [PP, PG, I32, P, P, P, P, P, P, P, P, P, P, S, P]
+    KV = ctypes.POINTER(hs_kv_quant)
+    lib.hs_kv_quant_write.argtypes = [PP, KV, PG, P, P, P, P, P]
+    lib.hs_kv_quant_read.argtypes = [PP, KV, PG, P, P, P, P, P]
+    lib.hs_sparse_attn_reuse_quant.argtypes = [PP, KV, PG, P, P, P, P, P, P]
+    lib.hs_decode_step_quant.argtypes = [PP, KV, PG, I32, P, P, P, P, P, P, P, P, S, P]
     lib.hs_status_string.argtypes = [I32]
     lib.hs_status_string.restype = ctypes.c_char_p
     lib.hs_launch_count.argtypes = []
@@ -206,6 +226,41 @@ def hs_decode_sparse_noalloc(p, q, k_cache, v_cache, seq_len, idx, idx_count, o,
            "hs_decode_sparse_noalloc")
 
 
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def hs_kv_quant_write(p, kv, pages, k, v, seq_len=None, n_new=None, stream=None):
+    """Quantise new rows k, v into the cache (include/hs.h); pages None: contiguous."""
+    _check(load().hs_kv_quant_write(_ref(p), _ref(kv), _ref(pages), _ptr(k), _ptr(v),
+                                    _ptr(seq_len), _ptr(n_new), _stream(stream)),
+           "hs_kv_quant_write")
+
+
+def hs_kv_quant_read(p, kv, pages, k, v, seq_len=None, n_new=None, stream=None):
+    """Read the rows that hs_kv_quant_write writes with these arguments back into k, v."""
+    _check(load().hs_kv_quant_read(_ref(p), _ref(kv), _ref(pages), _ptr(k), _ptr(v),
+                                   _ptr(seq_len), _ptr(n_new), _stream(stream)),
+           "hs_kv_quant_read")
+
+
+def hs_sparse_attn_reuse_quant(p, kv, pages, q_sparse, idx, idx_count, o_global, lse_global,
+                               stream=None):
+    _check(load().hs_sparse_attn_reuse_quant(_ref(p), _ref(kv), _ref(pages), _ptr(q_sparse),
+                                             _ptr(idx), _ptr(idx_count), _ptr(o_global),
+                                             _ptr(lse_global), _stream(stream)),
+           "hs_sparse_attn_reuse_quant")
+
+
+def hs_decode_step_quant(p, kv, pages, kind, q, seq_len, idx, idx_count, o, lse=None,
+                         sel_scores=None, workspace=None, stream=None):
+    wp, wb = _ws(workspace)
+    _check(load().hs_decode_step_quant(_ref(p), _ref(kv), _ref(pages), int(kind), _ptr(q),
+                                       _ptr(seq_len), _ptr(idx), _ptr(idx_count), _ptr(o),
+                                       _ptr(lse), _ptr(sel_scores), wp, wb, _stream(stream)),
+           "hs_decode_step_quant")
+
+
 def hs_workspace_size(p, which) -> int:
     n = load().hs_workspace_size(ctypes.byref(p), int(which))
     if n == ctypes.c_size_t(-1).value:
@@ -251,6 +306,18 @@ def full_outputs(p, device="cuda", with_scores=False):
     sel = (torch.empty(p.batch, p.hkv, p.t_q, p.ksel, dtype=torch.float32, device=device)
            if with_scores else None)
     return o, lse, idx, cnt, sel
+
+
+def kv_quant_cache(p, fmt, device="cuda", page_size=0, n_pages=0):
+    """Allocate the k_codes, k_scale, v_codes, v_scale of a quantised cache (zeros)."""
+    rows = (n_pages, p.hkv, page_size) if page_size else (p.batch, p.hkv, p.t_kv)
+    width = p.head_dim // 2 if fmt == "int4" else p.head_dim
+
+    def one():
+        return (torch.zeros(*rows, width, dtype=torch.uint8, device=device),
+                torch.zeros(*rows, 2, dtype=torch.bfloat16, device=device))
+
+    return (*one(), *one())
 
 
 def workspace(p, which, device="cuda"):
