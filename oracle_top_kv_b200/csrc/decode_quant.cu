@@ -1,23 +1,25 @@
 // decode_quant.cu -- decode step of the full layer over a quantised cache: it
 // attends to every cached row and selects the index set of the new token, as
-// decode_full.cu does over a bf16 cache, with other kernels:
+// decode_full.cu does over a bf16 cache.  Two kernels:
 //
-//  1. decode_quant_full_kernel: the caches' steps (32 4-bit or 16 8-bit keys
-//     each) of all (sequence, KV group) units, laid end to end, are cut into
-//     equal shares, one per CTA of a grid that fills the GPU once: ragged
-//     batches and few long sequences keep every SM busy alike.  A CTA writes
-//     one partial (m, l, O) per unit that its share touches.
-//  2. decode_quant_combine_kernel: exact log-sum-exp merge -> o, lse, lse2.
-//  3. decode_quant_select_kernel: the group score max_h (a2_h - lse2_h) needs
-//     every head's final lse.  Instead of carrying every logit from pass 1
-//     (64 bytes written and read per key against rows of 68 or 132) it reads the K rows
-//     again and recomputes the logits of its slice straight into shared memory,
-//     where the slice's top-(k - w) is found.  Its merge is decode_full.cu's.
-//  k - w > 1024: decode_quant_select_one_kernel, one CTA per unit.
-//  sel_scores: decode_quant_sel_scores_kernel rescores the selected keys.
+//  1. decode_quant_full_kernel.  The steps (32 or 16 keys) of all (sequence,
+//     KV group) units, laid end to end, are cut into equal shares, one per CTA
+//     of a grid that fills the GPU once: ragged batches and few long sequences
+//     keep every SM busy alike.  A CTA writes one partial (m, l, O) per unit
+//     that its share touches, and every step's largest logit per head.
+//  2. decode_quant_select_kernel, a cluster per unit: the exact log-sum-exp
+//     merge -> o, lse, then the index set.  The group score max_h (a2_h -
+//     lse2_h) of a key needs every head's final lse, so it cannot be ranked in
+//     pass 1.  Instead of carrying every logit over (64 bytes a key, against rows
+//     of 68 or 132), the maxima bound it: a tile of one step's keys has the
+//     largest score max_h (max_i a2_hi - lse2_h), exactly.  Each of the k - w best
+//     tiles (equal bounds: lower tile first) holds a key at least as good as
+//     every key of the others, so the k - w best keys lie in those tiles, and
+//     none is below the last one's bound.  Only they are read again (at most
+//     32 (k - w) keys), and of their keys only those that reach that bound are
+//     ranked.
 #include <atomic>
 
-#include "block_topk.cuh"
 #include "cta_select.cuh"
 #include "hs_common.cuh"
 #include "hs_kernels.cuh"
@@ -27,25 +29,29 @@ namespace hs {
 namespace dq {
 
 constexpr int kWarps = 4;
+constexpr int kStages = 3;
 constexpr int kMaxCtas = 640;  // partial slots reserved: at most kMaxCtas + units
-template <int F> constexpr int kStep = F == HS_KV_INT4 ? 32 : 16;
+template <int D, int F> using Attend = QAttend<D, F, kStages>;
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBoundCap = 16384;  // tile bounds a selecting CTA holds on chip
+template <int D, int F> using SelRing = QRing<D, F, false, 3>;
+
+constexpr int kBitsPad = 512;     // the tiles are dealt out in chunks of 32 to up to 8 CTAs
 
 struct Ws {
-    float* part;   // [kMaxCtas + units][kPart]
-    float* lse2;   // [batch * hq]
-    uint64_t* cand;
-    int* cand_n;
-    uint64_t* cand2;
-    int* cand2_n;
-    int n_sel, n_grp;
+    float* part;      // [kMaxCtas + units][32 + 16 D]
+    float* tmax;      // [units][tiles][16]: largest logit per head, log2 domain
+    uint32_t* bits;   // [units][tiles + kBitsPad]: bounds, where a CTA's exceed kBoundCap
+    int tiles;        // of t_kv, at the smallest step
     size_t bytes;
 };
 
 static Ws ws_layout(const KParams& p, void* base) {
     Ws w;
     const size_t units = (size_t)p.batch * p.hkv;
-    w.n_sel = sel_splits(p);
-    w.n_grp = sel_groups(w.n_sel);
+    w.tiles = (p.t_kv + 15) / 16;
     char* c = static_cast<char*>(base);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -54,11 +60,9 @@ static Ws ws_layout(const KParams& p, void* base) {
         return r;
     };
     w.part = (float*)take((kMaxCtas + units) * (32 + 16 * p.head_dim) * sizeof(float));
-    w.lse2 = (float*)take((size_t)p.batch * p.hq * sizeof(float));
-    w.cand = (uint64_t*)take(units * w.n_sel * kSelMaxRanked * sizeof(uint64_t));
-    w.cand_n = (int*)take(units * w.n_sel * sizeof(int));
-    w.cand2 = (uint64_t*)take(units * w.n_grp * kSelMaxRanked * sizeof(uint64_t));
-    w.cand2_n = (int*)take(units * w.n_grp * sizeof(int));
+    w.tmax = (float*)take(units * w.tiles * 16 * sizeof(float));
+    w.bits = (uint32_t*)take(w.tiles > kBoundCap ? units * (w.tiles + kBitsPad) * sizeof(uint32_t)
+                                                  : 0);
     w.bytes = at;
     return w;
 }
@@ -67,7 +71,7 @@ static Ws ws_layout(const KParams& p, void* base) {
 template <int NK>
 __device__ __forceinline__ int seq_steps(const int32_t* seq_len, int b, int t_kv) {
     const int L = __ldg(seq_len + b);
-    return L >= 1 && L <= t_kv ? (L + NK - 1) / NK : 0;
+    return L >= 1 && L <= t_kv ? (L - 1) / NK + 1 : 0;
 }
 
 // Sum over sequences b0 <= b < b1 of their steps, by one warp (all lanes get it).
@@ -92,14 +96,31 @@ __device__ __forceinline__ int share_of(long long x, int G, long long total) {
     return (int)(((x + 1) * G - 1) / total);
 }
 
+// Stores each step's maxima: lanes t = 0 of a warp hold a head pair each.
+struct TileMaxima {
+    float* at;  // this unit's [tiles][16]
+    __device__ __forceinline__ void operator()(int step, float m0, float m1) const {
+        const int lane = threadIdx.x & 31;
+        if ((lane & 3) == 0) {
+            float* r = at + (size_t)step * 16 + (lane >> 2);
+            r[0] = m0;
+            r[8] = m1;
+        }
+    }
+};
+
 template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     decode_quant_full_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
-                             const int32_t* __restrict__ seq_len, float* __restrict__ part) {
-    constexpr int NK = kStep<F>;
-    using A = QAttend<D, F, NK>;
-    extern __shared__ __align__(16) float smem[];  // kWarps partials
+                             const int32_t* __restrict__ seq_len, Ws ws) {
+    using A = Attend<D, F>;
+    constexpr int NK = A::NK;
+    extern __shared__ __align__(16) unsigned char smem_raw[];  // rings, reused for partials
+    constexpr int kStride = A::Ring::kBytes / 4;
+    static_assert(kStride >= A::kPart, "a partial fits a ring");
+    float* smem = reinterpret_cast<float*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = p.group;
+    const typename A::Ring ring{smem_u32(smem_raw) + warp * A::Ring::kBytes};
     const long long total = sum_steps<NK>(seq_len, 0, p.batch, p.t_kv) * p.hkv;
     const int G = ctas_used(gridDim.x, total);
     if (total == 0 || (int)blockIdx.x >= G) return;
@@ -133,24 +154,25 @@ __global__ void __launch_bounds__(kWarps * 32)
         const int s1 = (int)min((long long)n, s0 + (end - at));
         const int unit = b * p.hkv + u;
         A st;
-        st.init(q + ((size_t)b * p.hq + (size_t)u * g) * D, D, g);
+        st.init(q + ((size_t)b * p.hq + (size_t)u * g) * D, D, g, p.scale_log2);
         const QuantCache uc = unit_cache<D, F>(p, cache, unit);
         const int L = __ldg(seq_len + b);
-        if (p.bt) st.run(uc, QPagedRange{0, L, page_map(p, b, u)}, s0 + warp, kWarps, s1, p.scale_log2);
-        else st.run(uc, QRange{0, L}, s0 + warp, kWarps, s1, p.scale_log2);
+        const TileMaxima tm{ws.tmax + (size_t)unit * ws.tiles * 16};
+        if (p.bt) st.run(ring, uc, QPagedRange{0, L, page_map(p, b, u)}, s0 + warp, kWarps, s1, tm);
+        else st.run(ring, uc, QRange{0, L}, s0 + warp, kWarps, s1, tm);
         st.finish();
-        st.store_part(smem + warp * A::kPart, g);
+        st.store_part(smem + warp * kStride, g);
         __syncthreads();
-        float* dst = part + (size_t)(blockIdx.x + unit) * A::kPart;
+        float* dst = ws.part + (size_t)(blockIdx.x + unit) * A::kPart;
         for (int e = threadIdx.x; e < g * (D / 4); e += blockDim.x) {
             const int h = e / (D / 4);
             float M = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * A::kPart + 2 * h]);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * kStride + 2 * h]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float* pw = smem + w * A::kPart;
+                const float* pw = smem + w * kStride;
                 const float f = sq::merge_weight(pw[2 * h], M);
                 const float4 x = reinterpret_cast<const float4*>(pw + 32)[e];
                 l += pw[2 * h + 1] * f;
@@ -165,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                 dst[2 * h + 1] = l;
             }
         }
-        __syncthreads();  // the partials are read before the next unit's
+        __syncthreads();  // the partials are read before the rings fill again
         at += s1 - s0;
         s0 = 0;
         if (++u == p.hkv) {
@@ -175,328 +197,481 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-// One CTA per (sequence, head), `parts` x D threads: thread (part, d) adds up
-// element d of every parts-th partial of the unit.
-constexpr int kParts = 4;
-template <int D, int F>
-__global__ void __launch_bounds__(kParts * D)
-    decode_quant_combine_kernel(KParams p, const float* __restrict__ part, int grid,
-                                const int32_t* __restrict__ seq_len,
-                                __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
-                                float* __restrict__ lse2) {
-    constexpr int NK = kStep<F>, kPart = 32 + 16 * D;
-    __shared__ float s_acc[kParts][D], s_m[kParts * D / 32], s_l[kParts * D / 32];
-    const int row = blockIdx.x, h = row % p.hq, b = row / p.hq;
-    const int u = h / p.group, hh = h % p.group, unit = b * p.hkv + u;
-    const int tid = threadIdx.x, warp = tid >> 5, d = tid % D, prt = tid / D;
-    const int n = seq_steps<NK>(seq_len, b, p.t_kv);
-    if (n == 0) {  // length out of range
-        if (tid < D) o[(size_t)row * D + d] = __float2bfloat16_rn(0.f);
-        if (tid == 0) {
-            lse[row] = lse2[row] = -INFINITY;
-            set_status(HS_ERR_BOUNDS);
-        }
-        return;
-    }
-    const long long before = sum_steps<NK>(seq_len, 0, b, p.t_kv);
-    const long long total = (before + sum_steps<NK>(seq_len, b, p.batch, p.t_kv)) * p.hkv;
-    const long long first = before * p.hkv + (long long)u * n;
-    const int G = ctas_used(grid, total);
-    const int c0 = share_of(first, G, total), c1 = share_of(first + n - 1, G, total);
-    const float* base = part + (size_t)(c0 + unit) * kPart;
-    const int cnt = c1 - c0 + 1;
-    float M = -INFINITY;
-    for (int c = tid; c < cnt; c += kParts * D) M = fmaxf(M, base[(size_t)c * kPart + 2 * hh]);
-    M = warp_max(M);
-    if ((tid & 31) == 0) s_m[warp] = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kParts * D / 32; ++w) M = fmaxf(M, s_m[w]);
-    float l = 0.f, acc = 0.f;
-    for (int c = tid; c < cnt; c += kParts * D) {
-        const float* pc = base + (size_t)c * kPart;
-        l += pc[2 * hh + 1] * sq::merge_weight(pc[2 * hh], M);
-    }
-    l = warp_sum(l);
-    if ((tid & 31) == 0) s_l[warp] = l;
-#pragma unroll 4
-    for (int c = prt; c < cnt; c += kParts) {
-        const float* pc = base + (size_t)c * kPart;
-        acc += pc[32 + hh * D + d] * sq::merge_weight(pc[2 * hh], M);
-    }
-    s_acc[prt][d] = acc;
-    __syncthreads();
-    if (prt != 0) return;
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kParts * D / 32; ++w) l += s_l[w];
-#pragma unroll
-    for (int x = 1; x < kParts; ++x) acc += s_acc[x][d];
-    o[(size_t)row * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
-    if (d == 0) {
-        const float l2 = l == 0.f ? -INFINITY : M + log2f(l);
-        lse[row] = l2 * kLn2;
-        lse2[row] = l2;
-    }
+// ----------------------------------------------------------------- selection
+// Shared address `a` of cluster CTA `rank`, as a generic pointer.
+template <typename T>
+__device__ __forceinline__ T* cluster_ptr(T* a, int rank) {
+    T* r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(a), "r"(rank));
+    return r;
 }
 
-// -------------------------------------------------------------- group scores
-// Group scores of 16 keys by one warp, log2 domain: the keys are the 16 rows
-// (A) and the heads the columns (B), so a key's heads lie in one quad.
-template <int D, int F>
-struct QScore {
-    using R = QRow<D, F>;
-    uint32_t qb[2][D / 16][2];  // B fragments, heads 0..7 and 8..15
-    float qs[2][2], nl[2][2];   // heads 8 n + 2 t + e: scale_log2 sum(q), -lse2
-    float scale_log2;
-
-    __device__ __forceinline__ void init(const __nv_bfloat16* q, const float* lse2, int g,
-                                         float scale) {
-        const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-        scale_log2 = scale;
+// cta_kth_largest over the keys of all C CTAs of the cluster: get(0) ..
+// get(n - 1) are this CTA's.  All threads of all CTAs call; all get the result.
+template <typename Get>
+__device__ uint64_t cluster_kth_largest(Get get, int n, int k, CtaSelectSmem& sh, int C, int rank) {
+    if (C == 1) return cta_kth_largest(get, n, k, sh);
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+    CtaSelectSmem* root = cluster_ptr(&sh, 0);
+    uint64_t mn = ~0ull, mx = 0ull;
+    for (int i = tid; i < n; i += nt) {
+        const uint64_t v = get(i);
+        mn = v < mn ? v : mn;
+        mx = v > mx ? v : mx;
+    }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int h = 8 * n + gid;
-            __nv_bfloat16 x[D / 4];
-            const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)h * D + t * (D / 4));
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t a = shfl_xor_u64(mn, o), b = shfl_xor_u64(mx, o);
+        mn = a < mn ? a : mn;
+        mx = b > mx ? b : mx;
+    }
+    if (tid == 0) { sh.lo = ~0ull; sh.hi = 0ull; sh.found = 0ull; }
+    cluster_sync_all();
+    if (lane == 0 && mn <= mx) {
+        atomicMin(&root->lo, (unsigned long long)mn);
+        atomicMax(&root->hi, (unsigned long long)mx);
+    }
+    cluster_sync_all();
+    uint64_t lo = *(volatile unsigned long long*)&root->lo;
+    uint64_t hi = *(volatile unsigned long long*)&root->hi;
+    int need = k;
+    __shared__ uint64_t s_lo, s_hi;
+    __shared__ int s_need, s_single;
+    for (int pass = 0; pass < 9 && lo != hi; ++pass) {
+        const int shift = max(0, top_bit64(hi - lo) - 7);
+        for (int x = tid; x < 256; x += nt) sh.hist[x] = 0u;
+        __syncthreads();
+        for (int i = tid; i < n; i += nt) {
+            const uint64_t v = get(i);
+            if (v >= lo && v <= hi) atomicAdd(&sh.hist[(uint32_t)((v - lo) >> shift)], 1u);
+        }
+        cluster_sync_all();  // the root's histogram is zeroed and counted
+        if (rank != 0)
+            for (int x = tid; x < 256; x += nt)
+                if (sh.hist[x]) atomicAdd(&root->hist[x], sh.hist[x]);
+        cluster_sync_all();
+        if (tid < 32) {
+            uint32_t c[8], s = 0;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                reinterpret_cast<uint4*>(x)[i] = h < g ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            float sum = 0.f;
+            for (int j = 0; j < 8; ++j) {
+                c[j] = *(volatile uint32_t*)&root->hist[255 - 8 * lane - j];
+                s += c[j];
+            }
+            uint32_t incl = s;  // lane l owns buckets 255 - 8l .. 248 - 8l, from the top
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) sum += __bfloat162float(x[i]);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const __nv_bfloat162 pr =
-                        __halves2bfloat162(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
-                    qb[n][ks][e] = *reinterpret_cast<const uint32_t*>(&pr);
-                }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int hc = 8 * n + 2 * t + e;
-                qs[n][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4) * scale;
-                nl[n][e] = hc < g ? -lse2[hc] : -INFINITY;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const uint32_t excl = incl - s;
+            if (excl < (uint32_t)need && incl >= (uint32_t)need) {
+                uint32_t above = excl;
+                int j = 0;
+                while (above + c[j] < (uint32_t)need) { above += c[j]; ++j; }
+                const uint64_t nlo = lo + ((uint64_t)(255u - 8u * lane - j) << shift);
+                const uint64_t span = (1ull << shift) - 1ull;
+                s_lo = nlo;
+                s_hi = hi - nlo < span ? hi : nlo + span;
+                s_need = need - (int)above;
+                s_single = c[j] == 1u;
             }
         }
-    }
-    struct Regs {
-        uint32_t k[2][R::kKW], e[2];
-    };
-    // rows of keys gid and gid + 8 (-1: none)
-    __device__ __forceinline__ static void load(Regs& r, const QuantCache& c, int r0, int r1) {
-        const int t = threadIdx.x & 3;
-        ldg_words<R::kKW>(r.k[0], c.kc + (size_t)r0 * R::kBytes + t * (R::kBytes / 4), r0 >= 0);
-        ldg_words<R::kKW>(r.k[1], c.kc + (size_t)r1 * R::kBytes + t * (R::kBytes / 4), r1 >= 0);
-        r.e[0] = r0 >= 0 ? __ldg(c.ks + r0) : 0u;
-        r.e[1] = r1 >= 0 ? __ldg(c.ks + r1) : 0u;
-    }
-    // Scores of keys gid (.x) and gid + 8 (.y), the same in all lanes of a quad.
-    __device__ __forceinline__ float2 score(const Regs& r) const {
-        float s[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t a[4];
-            k_frag<F>(r.k[0], ks, a[0], a[2]);
-            k_frag<F>(r.k[1], ks, a[1], a[3]);
-            mma_bf16(s[0], a, qb[0][ks][0], qb[0][ks][1]);
-            mma_bf16(s[1], a, qb[1][ks][0], qb[1][ks][1]);
+        __syncthreads();
+        lo = s_lo;
+        hi = s_hi;
+        need = s_need;
+        const bool single = s_single != 0;
+        if (single && lo != hi) {  // the bucket holds one key: its CTA tells the others
+            for (int i = tid; i < n; i += nt) {
+                const uint64_t v = get(i);
+                if (v >= lo && v <= hi)
+                    for (int r = 0; r < C; ++r)
+                        *(volatile unsigned long long*)&cluster_ptr(&sh, r)->found = v;
+            }
+            cluster_sync_all();
+            return sh.found;
         }
-        float best[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float sc = entry_scale(r.e[k]);
-            float z = entry_zero(r.e[k]);
-            if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
-            const float s2 = sc * scale_log2;
-            float v = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    v = fmaxf(v, fmaf(s[n][2 * k + e], s2, qs[n][e] * z) + nl[n][e]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            best[k] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        }
-        return make_float2(best[0], best[1]);
+        cluster_sync_all();  // every CTA has read the root's histogram
+    }
+    return lo;
+}
+
+// Rows of listed tiles of NK keys (slot = place in the list * NK + key of the
+// tile), keys below `end` only.
+template <int NK>
+struct QTiles {
+    static constexpr bool kDirect = false;
+    const int* tiles;
+    int n_tiles, end;
+    bool paged;
+    PageMap pm;
+    __device__ __forceinline__ int key(int slot) const {
+        return slot < n_tiles * NK ? tiles[slot / NK] * NK + slot % NK : end;
+    }
+    __device__ __forceinline__ int row(int slot) const {
+        const int k = key(slot);
+        return k >= end ? -1 : paged ? pm.row(k) : k;
+    }
+};
+// The same of consecutive keys first ...
+struct QKeys {
+    static constexpr bool kDirect = false;
+    int first, end;
+    bool paged;
+    PageMap pm;
+    __device__ __forceinline__ int key(int slot) const { return first + slot; }
+    __device__ __forceinline__ int row(int slot) const {
+        const int k = first + slot;
+        return k >= end ? -1 : paged ? pm.row(k) : k;
     }
 };
 
-// Row of logical key `key` of unit (b, u), relative to unit_cache's bases.
-__device__ __forceinline__ int key_row(const KParams& p, const PageMap& pm, int key) {
-    return p.bt ? pm.row(key) : key;
-}
-
-// Scores of keys first .. first + n - 1, by all warps of the CTA, to
-// put(i, score) with i = 0 .. n - 1.
-template <int D, int F, class Put>
-__device__ __forceinline__ void score_keys(const QScore<D, F>& sc, const KParams& p,
-                                           const QuantCache& c, const PageMap& pm, int first, int n,
-                                           Put put) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    using S = QScore<D, F>;
-    auto row = [&](int i) { return i < n ? key_row(p, pm, first + i) : -1; };
-    typename S::Regs a, b;
-    int i = warp * 16;
-    if (i < n) S::load(a, c, row(i + gid), row(i + gid + 8));
-    for (; i < n; i += nw * 16) {
-        const int nx = i + nw * 16;
-        if (nx < n) S::load(b, c, row(nx + gid), row(nx + gid + 8));
-        const float2 v = sc.score(a);
-        const int k = i + gid + 8 * t;
-        if (t < 2 && k < n) put(k, t == 0 ? v.x : v.y);
-        a = b;
-    }
-}
-
-// Slice of the ranked keys 0..t-w of unit blockIdx.x / n_sel: its top-(k-w).
-template <int D, int F>
-__global__ void __launch_bounds__(kSelectThreads)
-    decode_quant_select_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
-                               const int32_t* __restrict__ seq_len, Ws ws) {
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ CtaSelectSmem cs;
-    __shared__ int s_n;
-    uint32_t* bits = reinterpret_cast<uint32_t*>(smem_raw);  // [kSelSlice]
-    const int unit = blockIdx.x / ws.n_sel, sp = blockIdx.x % ws.n_sel;
-    const int u = unit % p.hkv, b = unit / p.hkv;
-    const int L = seq_len[b];
-    const int Kc = p.k - p.window;
-    int* out_n = ws.cand_n + (size_t)unit * ws.n_sel + sp;
-    if (L < 1 || L > p.t_kv || L <= p.k || Kc <= 0) {  // nothing ranked here
-        if (threadIdx.x == 0) *out_n = 0;
-        return;
-    }
-    const int lo = L - p.window;  // ranked keys 0..lo-1
-    const int per = (lo + ws.n_sel - 1) / ws.n_sel;  // <= kSelSlice
-    const int i0 = sp * per;
-    const int n = max(0, min(lo, i0 + per) - i0);
-    const size_t head0 = (size_t)b * p.hq + (size_t)u * p.group;
-    QScore<D, F> sc;
-    sc.init(q + head0 * D, ws.lse2 + head0, p.group, p.scale_log2);
-    score_keys<D, F>(sc, p, unit_cache<D, F>(p, cache, unit), page_map(p, b, u), i0, n,
-                     [&](int i, float v) { bits[i] = float_order(v); });
-    __syncthreads();
-    auto key = [&](int i) -> uint64_t {
-        return ((uint64_t)bits[i] << 32) | (uint64_t)(0xffffffffu - (uint32_t)(i0 + i));
-    };
-    uint64_t* dst = ws.cand + ((size_t)unit * ws.n_sel + sp) * kSelMaxRanked;
-    if (n <= Kc) {
-        for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = key(i);
-        if (threadIdx.x == 0) *out_n = n;
-        return;
-    }
-    const uint64_t kth = cta_kth_largest(key, n, Kc, cs);
-    if (threadIdx.x == 0) s_n = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const uint64_t v = key(i);
-        if (v >= kth) dst[atomicAdd(&s_n, 1)] = v;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) *out_n = s_n;  // exactly Kc: the keys are distinct
-}
-
-// Budgets k - w above kSelMaxRanked: one CTA per unit streams the scores
-// through an exact top-k buffer.
-constexpr int kOneRound = kSelectThreads;  // keys offered per round
-template <int D, int F>
-__global__ void __launch_bounds__(kSelectThreads)
-    decode_quant_select_one_kernel(KParams p, QuantCache cache,
-                                   const __nv_bfloat16* __restrict__ q,
-                                   const int32_t* __restrict__ seq_len, Ws ws,
-                                   int32_t* __restrict__ idx, int32_t* __restrict__ cnt) {
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ int s_count;
-    __shared__ unsigned long long s_thresh;
-    __shared__ float s_score[kOneRound];
-    const int unit = blockIdx.x, u = unit % p.hkv, b = unit / p.hkv;
-    const int L = seq_len[b];
-    int32_t* irow = idx + (size_t)unit * p.ksel;
-    if (L < 1 || L > p.t_kv || L <= p.k) {  // no row, or the budget covers every key
-        const int n = L < 1 || L > p.t_kv ? 0 : L;
-        for (int x = threadIdx.x; x < p.ksel; x += blockDim.x) irow[x] = x < n ? x : -1;
-        if (threadIdx.x == 0) cnt[unit] = n;
-        return;
-    }
-    const int lo = L - p.window;
-    BlockTopK topk;
-    topk.setup(smem_raw, p.k - p.window, kOneRound, &s_count, &s_thresh);
-    const size_t head0 = (size_t)b * p.hq + (size_t)u * p.group;
-    QScore<D, F> sc;
-    sc.init(q + head0 * D, ws.lse2 + head0, p.group, p.scale_log2);
-    const QuantCache uc = unit_cache<D, F>(p, cache, unit);
-    const PageMap pm = page_map(p, b, u);
-    __syncthreads();
-    for (int i0 = 0; i0 < lo; i0 += kOneRound) {
-        const int n = min(kOneRound, lo - i0);
-        score_keys<D, F>(sc, p, uc, pm, i0, n, [&](int i, float v) { s_score[i] = v; });
-        __syncthreads();
-        if ((int)threadIdx.x < n) topk.offer(s_score[threadIdx.x], (uint32_t)(i0 + threadIdx.x));
-        topk.end_round();
-    }
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    const int n_out = topk.finish(irow, nullptr, p.ksel, lo, L - 1);
-    if (threadIdx.x == 0) cnt[unit] = n_out;
-}
-
-// sel_scores: max_h p of every selected key.
-template <int D, int F>
-__global__ void __launch_bounds__(128)
-    decode_quant_sel_scores_kernel(KParams p, QuantCache cache,
-                                   const __nv_bfloat16* __restrict__ q, const float* lse2,
-                                   const int32_t* __restrict__ idx,
-                                   const int32_t* __restrict__ cnt, float* __restrict__ sel) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
-    const int unit = blockIdx.x, u = unit % p.hkv, b = unit / p.hkv;
-    const size_t head0 = (size_t)b * p.hq + (size_t)u * p.group;
-    const int n = cnt[unit];
-    QScore<D, F> sc;
-    sc.init(q + head0 * D, lse2 + head0, p.group, p.scale_log2);
-    const QuantCache uc = unit_cache<D, F>(p, cache, unit);
-    const PageMap pm = page_map(p, b, u);
-    const int32_t* irow = idx + (size_t)unit * p.ksel;
-    for (int i = 16 * (blockIdx.y * 4 + warp); i < p.ksel; i += 64 * gridDim.y) {
-        int r[2];
+// Rescores a source's keys, warp w of the CTA steps w, w + kSelWarps, ...: put(key,
+// score, log2 domain) for each; after_round() once per round, by all threads.
+template <int D, int F, class Src, class Put, class After>
+__device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&lse2)[2],
+                                           uint32_t ring_base, const QuantCache& c, const Src& src,
+                                           int n_steps, Put put, After after_round) {
+    using Ring = SelRing<D, F>;
+    constexpr int NK = Ring::NK;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const Ring ring{ring_base + warp * Ring::kBytes};
+    auto mine = [&](int st) { return st < n_steps ? src.row(st * NK + (lane & (NK - 1))) : -1; };
+    int row = mine(warp), ahead = warp;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int x = i + gid + 8 * k;
-            r[k] = x < n ? key_row(p, pm, irow[x]) : -1;
+    for (int i = 0; i < 2; ++i) {
+        if (ahead < n_steps) ring.fill(i, c, src, ahead * NK, row);
+        cp_async_commit();
+        ahead += kSelWarps;
+        row = mine(ahead);
+    }
+    int s = 0;
+    for (int r0 = 0; r0 < n_steps; r0 += kSelWarps) {
+        const int st = r0 + warp;
+        cp_async_wait<1>();
+        __syncwarp();
+        if (ahead < n_steps) ring.fill(s == 0 ? 2 : s - 1, c, src, ahead * NK, row);
+        cp_async_commit();
+        ahead += kSelWarps;
+        row = mine(ahead);
+        if (st < n_steps) {
+            const uint32_t live = ring.live(s, src, st * NK);
+            float x[NK / 4][2];
+            q.logits(x, ring, s, live);
+#pragma unroll
+            for (int i = 0; i < NK / 16; ++i) {
+                // v[je]: key t + 4 je of the group, this lane's two heads; then the
+                // maximum over gid, each halving of the lanes dropping half the keys
+                float v[4];
+#pragma unroll
+                for (int je = 0; je < 4; ++je) {
+                    const float(&y)[2] = x[4 * i + je];
+                    v[je] = fmaxf(fmaxf(-INFINITY, __fsub_rn(__fmul_rn(y[0], q.kf[0]), lse2[0])),
+                                  __fsub_rn(__fmul_rn(y[1], q.kf[1]), lse2[1]));
+                }
+                const bool up = lane & 16, up2 = lane & 8;
+                const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+                const float b = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+                const float w0 = fmaxf(up ? v[2] : v[0], a), w1 = fmaxf(up ? v[3] : v[1], b);
+                const float d = __shfl_xor_sync(0xffffffffu, up2 ? w0 : w1, 8);
+                float e = fmaxf(up2 ? w1 : w0, d);
+                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4));
+                const int slot = 16 * i + t + 4 * (2 * (up ? 1 : 0) + (up2 ? 1 : 0));
+                if (!(lane & 4) && ((live >> slot) & 1u)) put(src.key(st * NK + slot), e);
+            }
         }
-        typename QScore<D, F>::Regs regs;
-        QScore<D, F>::load(regs, uc, r[0], r[1]);
-        const float2 v = sc.score(regs);
-        const int x = i + gid + 8 * t;
-        if (t < 2 && x < p.ksel)
-            sel[(size_t)unit * p.ksel + x] = x < n ? exp2f(t == 0 ? v.x : v.y) : 0.f;
+        s = s == 2 ? 0 : s + 1;
+        after_round();
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+}
+
+// Keeps the K largest of buf[0..n) (n > K), in buf[0..K); tmp holds K keys.
+__device__ void keep_largest(uint64_t* buf, int n, int K, uint64_t* tmp, CtaSelectSmem& cs,
+                             int* s_n, uint64_t* kth_out) {
+    const uint64_t kth = cta_kth_largest([&](int i) { return buf[i]; }, n, K, cs);
+    if (threadIdx.x == 0) *s_n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (buf[i] >= kth) tmp[atomicAdd(s_n, 1)] = buf[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < K; i += blockDim.x) buf[i] = tmp[i];
+    __syncthreads();
+    *kth_out = kth;
+}
+
+// Dynamic shared memory of the selection, for Kc = k - w.
+template <int D, int F>
+struct SelSmem {
+    static constexpr size_t kFront =  // rings; before that, tile bounds or the merge's sums
+        (size_t)kSelWarps * SelRing<D, F>::kBytes > sizeof(uint32_t) * kBoundCap
+            ? (size_t)kSelWarps * SelRing<D, F>::kBytes
+            : sizeof(uint32_t) * kBoundCap;
+    static constexpr int kRound = kSelWarps * SelRing<D, F>::NK;  // keys offered per round
+    __host__ __device__ static int cap(int Kc) { return 2 * Kc + kRound; }
+    __host__ __device__ static int sort_n(int Kc) { return next_pow2(Kc > 0 ? Kc : 1); }
+    __host__ __device__ static size_t bytes(int Kc) {
+        return kFront + sizeof(uint64_t) * (cap(Kc) + sort_n(Kc)) + sizeof(int) * (Kc + 2);
+    }
+};
+
+template <int D, int F>
+__global__ void __launch_bounds__(kSelThreads, 1)
+    decode_quant_select_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
+                               const int32_t* __restrict__ seq_len, Ws ws, int grid1, int C,
+                               __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                               int32_t* __restrict__ idx, int32_t* __restrict__ cnt,
+                               float* __restrict__ sel) {
+    using A = Attend<D, F>;
+    using S = SelSmem<D, F>;
+    constexpr int NK = A::NK;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __shared__ CtaSelectSmem cs;
+    __shared__ float s_m[16], s_lse2[16];
+    __shared__ int s_n, s_list, s_cut;
+    __shared__ unsigned long long s_thr;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, g = p.group;
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / C, u = unit % p.hkv, b = unit / p.hkv;
+    const int L = __ldg(seq_len + b);
+    const size_t head0 = (size_t)b * p.hq + (size_t)u * g;
+    int32_t* irow = idx + (size_t)unit * p.ksel;
+    float* srow = sel ? sel + (size_t)unit * p.ksel : nullptr;
+    const int n = seq_steps<NK>(seq_len, b, p.t_kv);
+    if (n == 0) {  // length out of range: nothing attended, nothing selected
+        if (rank != 0) return;
+        for (int x = tid; x < g * D; x += blockDim.x) o[head0 * D + x] = __float2bfloat16_rn(0.f);
+        for (int x = tid; x < g; x += blockDim.x) lse[head0 + x] = -INFINITY;
+        for (int x = tid; x < p.ksel; x += blockDim.x) {
+            irow[x] = -1;
+            if (srow) srow[x] = 0.f;
+        }
+        if (tid == 0) { cnt[unit] = 0; set_status(HS_ERR_BOUNDS); }
+        return;
+    }
+    // ---- merge of the unit's partials
+    {
+        const long long before = sum_steps<NK>(seq_len, 0, b, p.t_kv);
+        const long long total = (before + sum_steps<NK>(seq_len, b, p.batch, p.t_kv)) * p.hkv;
+        const long long first = before * p.hkv + (long long)u * n;
+        const int G = ctas_used(grid1, total);
+        const int c0 = share_of(first, G, total), parts = share_of(first + n - 1, G, total) - c0 + 1;
+        const float* base = ws.part + (size_t)(c0 + unit) * A::kPart;
+        if (warp < g) {
+            float M = -INFINITY, l = 0.f;
+            for (int c = lane; c < parts; c += 32) M = fmaxf(M, base[(size_t)c * A::kPart + 2 * warp]);
+            M = warp_max(M);
+            for (int c = lane; c < parts; c += 32) {
+                const float* pc = base + (size_t)c * A::kPart + 2 * warp;
+                l += pc[1] * sq::merge_weight(pc[0], M);
+            }
+            l = warp_sum(l);
+            if (lane == 0) {
+                const float l2 = l == 0.f ? -INFINITY : M + log2f(l);
+                s_m[warp] = M;
+                s_lse2[warp] = l2;
+                if (warp % C == rank) lse[head0 + warp] = l2 * kLn2;
+            }
+        }
+        __syncthreads();
+        // heads rank, rank + C, ...: each float4 of their outputs by `per` threads
+        const int heads = (g - rank + C - 1) / C, items = max(0, heads) * (D / 4);
+        float4* red = reinterpret_cast<float4*>(smem_raw);  // [kSelThreads]
+        int per = 1;
+        while (2 * per * items <= kSelThreads && per < parts) per *= 2;
+        for (int i0 = 0; i0 < items; i0 += kSelThreads / per) {
+            const int it = i0 + tid / per, pr = tid % per;
+            const int h = (it / (D / 4)) * C + rank, d4 = it % (D / 4);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (it < items) {
+                const float M = s_m[h];
+#pragma unroll 4
+                for (int c = pr; c < parts; c += per) {
+                    const float* pc = base + (size_t)c * A::kPart;
+                    const float f = sq::merge_weight(pc[2 * h], M);
+                    const float4 x = reinterpret_cast<const float4*>(pc + 32 + h * D)[d4];
+                    acc.x += x.x * f;
+                    acc.y += x.y * f;
+                    acc.z += x.z * f;
+                    acc.w += x.w * f;
+                }
+            }
+            red[tid] = acc;
+            __syncthreads();
+            if (it < items && pr == 0) {
+                for (int x = 1; x < per; ++x) {
+                    const float4 y = red[tid + x];
+                    acc.x += y.x;
+                    acc.y += y.y;
+                    acc.z += y.z;
+                    acc.w += y.w;
+                }
+                // sum p = 2^(lse2 - M); no key: both sums are 0
+                const float inv = s_m[h] == -INFINITY && acc.x == 0.f ? 0.f : exp2f(s_m[h] - s_lse2[h]);
+                *reinterpret_cast<uint2*>(o + (head0 + h) * D + 4 * d4) = make_uint2(
+                    pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            }
+            __syncthreads();
+        }
+    }
+    // ---- the index set
+    const int Kc = p.k - p.window;
+    const bool ranked = L > p.k && Kc > 0;
+    const int lo = L > p.k ? L - p.window : 0;  // keys lo.. are all selected
+    if (!ranked && rank != 0) return;
+    const QuantCache uc = unit_cache<D, F>(p, cache, unit);
+    const PageMap pm = page_map(p, b, u);
+    const bool paged = p.bt != nullptr;
+    uint64_t* buf = reinterpret_cast<uint64_t*>(smem_raw + S::kFront);  // [cap(Kc)]
+    uint64_t* tmp = buf + S::cap(Kc);                                    // [sort_n(Kc)]
+    int* list = reinterpret_cast<int*>(tmp + S::sort_n(Kc));             // [Kc + 2]
+    QQuery<D, F> qq;
+    float nl[2];
+    if (ranked || srow) {
+        qq.init(q + head0 * D, D, g, p.scale_log2);
+        nl[0] = gid < g ? s_lse2[gid] : INFINITY;
+        nl[1] = gid + 8 < g ? s_lse2[gid + 8] : INFINITY;
+    }
+    if (tid == 0) { s_n = 0; s_list = 0; s_thr = 0ull; }
+    __syncthreads();
+    int n_best = 0;
+    if (ranked) {
+        const int full = lo / NK;  // tiles of ranked keys only; tile `full` has some if lo % NK
+        // this CTA's tiles: chunks of 32, dealt out over the cluster
+        const int chunks = (full + 31) / 32;
+        const int mine = (chunks > rank ? (chunks - rank - 1) / C + 1 : 0) * 32;
+        auto tile = [&](int i) { return ((i >> 5) * C + rank) * 32 + (i & 31); };
+        if (full <= Kc) {
+            for (int i = tid; i < mine; i += blockDim.x)
+                if (tile(i) < full) list[atomicAdd(&s_list, 1)] = tile(i);
+        } else {
+            const float4* tm = reinterpret_cast<const float4*>(ws.tmax + (size_t)unit * ws.tiles * 16);
+            uint32_t* bits = mine <= kBoundCap ? reinterpret_cast<uint32_t*>(smem_raw)
+                                               : ws.bits + (size_t)unit * (ws.tiles + kBitsPad) +
+                                                     (size_t)rank * ((chunks + C - 1) / C) * 32;
+            // a CTA may hold up to 31 places past its tiles: they rank last
+            for (int i = tid; i < mine; i += blockDim.x) {
+                const int x = tile(i);
+                float v = -INFINITY;
+                if (x < full) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        if (4 * q4 >= g) break;
+                        const float4 a = __ldg(tm + (size_t)x * 4 + q4);
+                        const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (4 * q4 + e < g) v = fmaxf(v, __fsub_rn(av[e], s_lse2[4 * q4 + e]));
+                    }
+                }
+                bits[i] = x < full ? float_order(v) : 0u;
+            }
+            __syncthreads();
+            auto key = [&](int i) -> uint64_t {
+                return ((uint64_t)bits[i] << 32) | (uint64_t)(0xffffffffu - (uint32_t)tile(i));
+            };
+            const uint64_t kth = cluster_kth_largest(key, mine, Kc, cs, C, rank);
+            for (int i = tid; i < mine; i += blockDim.x)
+                if (key(i) >= kth) list[atomicAdd(&s_list, 1)] = tile(i);
+            if (tid == 0) {
+                // the bounds and the scores below are the same arithmetic on the same
+                // operands; the step down covers a difference in their last bits
+                const float th = sel_key_score(kth);
+                float mag = fabsf(th);
+                for (int h = 0; h < g; ++h) mag = fmaxf(mag, fabsf(s_lse2[h]));
+                s_thr = isfinite(mag) ? (uint64_t)float_order(th - 4e-6f * mag) << 32 : 0ull;
+            }
+        }
+        __syncthreads();
+        if (tid == 0 && rank == 0 && lo % NK != 0) list[s_list++] = full;
+        __syncthreads();
+        const QTiles<NK> src{list, s_list, lo, paged, pm};
+        const int cap = S::cap(Kc);
+        score_keys<D, F>(
+            qq, nl, smem_u32(smem_raw), uc, src, s_list,
+            [&](int key, float v) {
+                const uint64_t c = sel_key(v, (uint32_t)key);
+                if (c >= s_thr) buf[atomicAdd(&s_n, 1)] = c;
+            },
+            [&] {
+                __syncthreads();
+                const int have = s_n;
+                __syncthreads();  // read by all before the next offers
+                if (have > cap - S::kRound) {
+                    uint64_t kth;
+                    keep_largest(buf, have, Kc, tmp, cs, &s_cut, &kth);
+                    if (tid == 0) { s_thr = kth; s_n = Kc; }
+                    __syncthreads();
+                }
+            });
+        __syncthreads();
+        n_best = s_n;
+        uint64_t kth;
+        if (n_best > Kc) {
+            keep_largest(buf, n_best, Kc, tmp, cs, &s_cut, &kth);
+            n_best = Kc;
+        }
+        if (C > 1) {
+            if (tid == 0) s_n = n_best;
+            cluster_sync_all();
+            if (rank == 0)
+                for (int r = 1; r < C; ++r) {
+                    const int m = *(volatile int*)cluster_ptr(&s_n, r);
+                    const volatile uint64_t* from = cluster_ptr(buf, r);
+                    for (int x = tid; x < m; x += blockDim.x) buf[n_best + x] = from[x];
+                    __syncthreads();
+                    n_best += m;
+                    if (n_best > Kc) {
+                        keep_largest(buf, n_best, Kc, tmp, cs, &s_cut, &kth);
+                        n_best = Kc;
+                    }
+                }
+            cluster_sync_all();  // the others keep their buffers until here
+            if (rank != 0) return;
+        }
+        const int sort_n = next_pow2(max(n_best, 1));
+        for (int x = tid; x < sort_n; x += blockDim.x)
+            tmp[x] = x < n_best ? ((uint64_t)sel_key_id(buf[x]) << 32) | (buf[x] >> 32) : ~0ull;
+        __syncthreads();
+        cta_bitonic_sort(tmp, sort_n);
+        for (int x = tid; x < n_best; x += blockDim.x) {
+            irow[x] = (int32_t)(tmp[x] >> 32);
+            if (srow) srow[x] = exp2f(order_float((uint32_t)tmp[x]));
+        }
+    }
+    for (int x = tid; x < L - lo; x += blockDim.x) irow[n_best + x] = lo + x;
+    const int n_out = n_best + L - lo;
+    for (int x = n_out + tid; x < p.ksel; x += blockDim.x) {
+        irow[x] = -1;
+        if (srow) srow[x] = 0.f;
+    }
+    if (tid == 0) cnt[unit] = n_out;
+    if (srow) {
+        __syncthreads();
+        score_keys<D, F>(
+            qq, nl, smem_u32(smem_raw), uc, QKeys{lo, L, paged, pm}, (L - lo + NK - 1) / NK,
+            [&](int key, float v) { srow[n_best + key - lo] = exp2f(v); }, [] {});
     }
 }
 
-// CTAs of the full kernel that fill the current device once (cached per device).
+// CTAs of the full kernel that fill the current device once, and its SMs
+// (cached per device).
 template <int D, int F>
-static cudaError_t full_grid(size_t smem, int* ctas) {
+static cudaError_t full_grid(size_t smem, int* ctas, int* sms) {
     static std::atomic<int> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
     int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        int sms = 0, per = 0;
-        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-            return e;
+        int per = 0;
         if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                  &per, decode_quant_full_kernel<D, F>, kWarps * 32, smem)) != cudaSuccess)
             return e;
-        n = min(kMaxCtas, max(1, per) * sms);
+        n = min(kMaxCtas, max(1, per) * *sms);
         if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     }
     *ctas = n;
@@ -507,67 +682,51 @@ template <int D, int F>
 static cudaError_t launch_t(const KParams& p, const QuantCache& c, const void* q_,
                             const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,
                             float* lse, float* sel, void* ws_, cudaStream_t st) {
-    using A = QAttend<D, F, kStep<F>>;
+    using A = Attend<D, F>;
     const __nv_bfloat16* q = (const __nv_bfloat16*)q_;
     const Ws w = ws_layout(p, ws_);
     const int units = p.batch * p.hkv;
     cudaError_t e;
     auto full = decode_quant_full_kernel<D, F>;
-    const size_t smem = kWarps * A::kPart * sizeof(float);
+    const size_t smem = (size_t)kWarps * A::Ring::kBytes;
     if ((e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
         cudaSuccess)
         return e;
-    int G = 0;
-    if ((e = full_grid<D, F>(smem, &G)) != cudaSuccess) return e;
+    int G = 0, sms = 148;
+    if ((e = full_grid<D, F>(smem, &G, &sms)) != cudaSuccess) return e;
     // no CTA below a step per warp, as far as the capacity tells
-    const long long most = (long long)units * ((p.t_kv + kStep<F> - 1) / kStep<F>);
-    G = (int)max(1ll, min((long long)G, (most + kWarps - 1) / kWarps));
-    full<<<G, kWarps * 32, smem, st>>>(p, c, q, seq_len, w.part);
+    const int steps = (p.t_kv + A::NK - 1) / A::NK;
+    G = (int)max(1ll, min((long long)G, ((long long)units * steps + kWarps - 1) / kWarps));
+    full<<<G, kWarps * 32, smem, st>>>(p, c, q, seq_len, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    decode_quant_combine_kernel<D, F><<<p.batch * p.hq, kParts * D, 0, st>>>(
-        p, w.part, G, seq_len, (__nv_bfloat16*)o, lse, w.lse2);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int Kc = p.k - p.window;
-    if (Kc <= kSelMaxRanked) {
-        auto select = decode_quant_select_kernel<D, F>;
-        const size_t s1 = sizeof(uint32_t) * kSelSlice;
-        if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)s1)) != cudaSuccess)
-            return e;
-        select<<<units * w.n_sel, kSelectThreads, s1, st>>>(p, c, q, seq_len, w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        DecodeWs d = {};
-        d.lse2 = w.lse2;
-        d.cand = w.cand;
-        d.cand_n = w.cand_n;
-        d.cand2 = w.cand2;
-        d.cand2_n = w.cand2_n;
-        d.n_sel = w.n_sel;
-        d.n_grp = w.n_grp;
-        if ((e = launch_select_merge(p, d, seq_len, idx, cnt, nullptr, st)) != cudaSuccess) return e;
-    } else {
-        auto one = decode_quant_select_one_kernel<D, F>;
-        const size_t s1 = BlockTopK::smem_bytes(Kc, kOneRound);
-        if ((e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)s1)) != cudaSuccess)
-            return e;
-        one<<<units, kSelectThreads, s1, st>>>(p, c, q, seq_len, w, idx, cnt);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (sel)
-        decode_quant_sel_scores_kernel<D, F><<<dim3(units, 8), 128, 0, st>>>(p, c, q, w.lse2, idx,
-                                                                            cnt, sel);
-    return cudaGetLastError();
+    auto select = decode_quant_select_kernel<D, F>;
+    const size_t s1 = SelSmem<D, F>::bytes(p.k - p.window);
+    if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) !=
+        cudaSuccess)
+        return e;
+    // clusters as wide as a wave of one CTA per SM allows, while a CTA still
+    // has more than 8 chunks of tiles
+    int C = 1;
+    while (C < 8 && units * C * 2 <= sms && steps / (C * 2) > 256) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(units * C));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = s1;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, select, p, c, q, seq_len, w, G, C, (__nv_bfloat16*)o, lse, idx,
+                              cnt, sel);
 }
 
 }  // namespace dq
 
 size_t decode_quant_workspace(const KParams& p) { return dq::ws_layout(p, nullptr).bytes; }
-
-int decode_quant_kernel_count(const KParams& p, bool sel) {
-    const int select = p.k - p.window > kSelMaxRanked ? 1 : sel_groups(sel_splits(p)) > 0 ? 3 : 2;
-    return 2 + select + (sel ? 1 : 0);
-}
 
 cudaError_t launch_decode_quant(const KParams& p, int format, const QuantCache& c, const void* q,
                                 const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,

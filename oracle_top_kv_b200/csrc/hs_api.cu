@@ -449,7 +449,7 @@ hs_status hs_decode_step_quant(const hs_params* p, const hs_kv_quant* kv, const 
     if (!lse) return HS_ERR_INVALID_ARG;
     if (workspace == nullptr || ws_bytes < hs::decode_quant_workspace(kp) || !aligned16(workspace))
         return HS_ERR_WORKSPACE;
-    return launched(hs::decode_quant_kernel_count(kp, sel_scores != nullptr), [&] {
+    return launched(2, [&] {
         return hs::launch_decode_quant(kp, kv->format, c, q, seq_len, idx, idx_count, o, lse,
                                        sel_scores, workspace, st);
     });

@@ -134,7 +134,6 @@ cudaError_t launch_decode_sparse_quant(const KParams& p, int format, const Quant
                                        const void* q, const int32_t* seq_len, const int32_t* idx,
                                        const int32_t* cnt, void* o, float* lse, cudaStream_t st);
 size_t decode_quant_workspace(const KParams& p);
-int decode_quant_kernel_count(const KParams& p, bool sel);
 cudaError_t launch_decode_quant(const KParams& p, int format, const QuantCache& c, const void* q,
                                 const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,
                                 float* lse, float* sel, void* ws, cudaStream_t st);

@@ -7,21 +7,36 @@
 // e4m3 number, one byte per element.
 //
 // Attention never rebuilds the values.  For a key with entry (s, z),
-//     scale q.k^ = tau (s (q.c') + z' sum(q)),
+//     scale q.k^ = scale (s (q.c') + z' sum(q)),
 //     sum_i p_i v^_i = sum_i (p_i s_i) c'_i + sum_i p_i z'_i,
 // with c' = c - 8, z' = z + 8 s in 4 bits and c' = c, z' = z in 8.  c' is exact in
-// bf16, so both products run on codes, and scale and zero are applied to the
-// logits, to P and to one running sum per head: two roundings fewer than with
-// rows rebuilt in bf16 first, and no multiply per element.  p_i s_i is rounded
-// to bf16 for its product (relative 2^-9, as the bf16 kernels round p_i);
-// everything else is fp32.
+// fp16, so both products run on codes in fp16 MMAs with fp32 accumulators, and
+// scale and zero are applied to the logits, to P and to one running sum per
+// head.  fp16 rather than bf16: two of a half-word's four nibbles turn into
+// fp16 without a shift, and e4m3 has a conversion instruction; integer and
+// logic instructions issue every other cycle and were what bounded a bf16
+// form of this (33% of issue slots, half of them on that pipe).  What fp16's
+// range needs:
+//  - q is scaled by a power of two per head so that max|q| lies in [2^14, 2^15);
+//    a bf16 element is then exact unless it is 2^-29 of the largest or less
+//    (error 2^-39 of the largest);
+//  - p_i s_i is taken relative to 2^10 at the running maximum (growing to
+//    2^14 before O is rescaled) and to a power of two above the largest |s_i|
+//    seen, and rounded to fp16: relative 2^-12 for weights down to 2^-24 of the
+//    largest, an absolute 2^-35 of it below.
+// Everything else is fp32.
 //
-// One warp, 16 heads as the rows of mma.m16n8k16.  Lane (gid, t) of the warp
-// (gid = lane / 4, t = lane % 4) reads straight from the cache what its
-// fragments need, with no pass through shared memory: of key gid of an 8-key
-// tile the t-th quarter of the row (Q's fragments take the same order of
-// dimensions), and of the V rows of keys 2t and 2t + 1 the gid-th eighth.
+// One warp, 16 heads as the rows of mma.m16n8k16, 16 keys at a time.  Lane
+// (gid, t) of the warp (gid = lane / 4, t = lane % 4) needs of a key's K row the
+// t-th quarter and of a V row the gid-th eighth (Q's fragments take the same
+// order of dimensions), so rows are read from shared memory as they lie in the
+// cache.  cp.async fills a ring of stages per warp; it also places the rows:
+// within 16 keys, key t + 4 e + 8 j is column 2 t + e of 8-column tile j, K rows lie in
+// column order, V rows keep their order with 16-byte chunks swizzled, a lane's
+// four entries are adjacent: every shared read is free of bank conflicts.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "attend_mma.cuh"
 #include "hs_common.cuh"
@@ -45,63 +60,52 @@ struct QRow {
     static constexpr int kVW = kBytes / 32;  // words of an eighth row
 };
 
-template <int N>
-__device__ __forceinline__ void ldg_words(uint32_t (&w)[N], const uint8_t* p, bool ok) {
-    if (!ok) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = 0u;
-        return;
-    }
-    if constexpr (N == 1) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else if constexpr (N == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-            w[i] = v.x;
-            w[i + 1] = v.y;
-            w[i + 2] = v.z;
-            w[i + 3] = v.w;
-        }
-    }
-}
-
 __device__ __forceinline__ float entry_scale(uint32_t e) { return __uint_as_float(e << 16); }
 __device__ __forceinline__ float entry_zero(uint32_t e) { return __uint_as_float(e & 0xffff0000u); }
 
-__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                     *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// D = A(16x16 fp16, row) * B(16x8 fp16, col) + D (fp32)
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                     *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
-// Two 4-bit codes, in the low nibbles of x's halves, as bf16 pair c - 8:
-// 0x4300 | c is the bf16 number 128 + c, and the subtraction is exact.
+// The 4-bit codes in bits 0..3 (nibble 0) or 4..7 (nibble 1) of x's halves, as an
+// fp16 pair c - 8: 0x6400 | c is the fp16 number 1024 + c, 0x6400 | 16 c is
+// 1024 + 16 c, and both steps back are exact.
+template <int NIBBLE>
 __device__ __forceinline__ uint32_t int4_pair(uint32_t x) {
-    return bf2_sub((x & 0x000f000fu) | 0x43004300u, 0x43084308u);
+    if constexpr (NIBBLE == 0)
+        return as_u32(__hsub2(as_half2((x & 0x000f000fu) | 0x64006400u), as_half2(0x64086408u)));
+    else
+        return as_u32(__hfma2(as_half2((x & 0x00f000f0u) | 0x64006400u), as_half2(0x2c002c00u),
+                              as_half2(0xd480d480u)));
 }
-// Two e4m3 codes, in the high bytes of x's halves, as a bf16 pair: sign, exponent
-// and mantissa moved to bf16's places give the number times 2^-120 (subnormals
-// too), and the product with 2^120 is exact.
+// The two e4m3 codes in the low half of x as an fp16 pair (exact).
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t x) {
-    return bf2_mul(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), 0x7b807b80u);
+    uint32_t r;
+    asm("{.reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
+    return r;
 }
 
 // Dimension (of a quarter row) that element e (0: b0 low, 1: b0 high, 2: b1
 // low, 3: b1 high) of k step `ks` holds.
 template <int F>
 __host__ __device__ constexpr int k_dim(int ks, int e) {
-    return F == HS_KV_INT4 ? 8 * (ks >> 1) + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1)
-                           : 4 * ks + (e >> 1) + 2 * (e & 1);
+    return F == HS_KV_INT4 ? 8 * (ks >> 1) + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1) : 4 * ks + e;
 }
 
 // B fragment (b0, b1) of k step `ks` from a lane's quarter of a K row.
@@ -109,23 +113,28 @@ template <int F, int N>
 __device__ __forceinline__ void k_frag(const uint32_t (&w)[N], int ks, uint32_t& b0, uint32_t& b1) {
     if constexpr (F == HS_KV_INT4) {
         const uint32_t x = w[ks >> 1] >> (8 * (ks & 1));
-        b0 = int4_pair(x);
-        b1 = int4_pair(x >> 4);
+        b0 = int4_pair<0>(x);
+        b1 = int4_pair<1>(x);
     } else {
-        b0 = fp8_pair(w[ks] << 8);
-        b1 = fp8_pair(w[ks]);
+        b0 = fp8_pair(w[ks]);
+        b1 = fp8_pair(w[ks] >> 16);
     }
 }
 
-// The pair (a[j], b[j]) of element j of two lanes' eighths of V rows.
+// Pairs (a[j], b[j]) and (a[j + 1], b[j + 1]) of a lane's eighths of two V rows,
+// j even.
 template <int F, int N>
-__device__ __forceinline__ uint32_t v_pair(const uint32_t (&a)[N], const uint32_t (&b)[N], int j) {
+__device__ __forceinline__ void v_pairs(const uint32_t (&a)[N], const uint32_t (&b)[N], int j,
+                                        uint32_t& p0, uint32_t& p1) {
     if constexpr (F == HS_KV_INT4) {
-        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7632 : 0x5410);
-        return int4_pair(x >> (4 * (j & 3)));
+        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7632 : 0x5410) >>
+                           (4 * (j & 2));
+        p0 = int4_pair<0>(x);
+        p1 = int4_pair<1>(x);
     } else {
-        const int i = j & 3;  // bytes (any, a_i, any, b_i)
-        return fp8_pair(__byte_perm(a[j >> 2], b[j >> 2], (i << 4) | ((4 + i) << 12)));
+        const uint32_t x = __byte_perm(a[j >> 2], b[j >> 2], (j & 2) ? 0x7362 : 0x5140);
+        p0 = fp8_pair(x);
+        p1 = fp8_pair(x >> 16);
     }
 }
 
@@ -173,49 +182,248 @@ struct QIndex {
     }
 };
 
-// ---------------------------------------------------------------- attention
-// NK: keys of one step of a warp (16 or 32).
-template <int D, int F, int NK>
-struct QAttend {
+// -------------------------------------------------------------- ring of rows
+// A warp's stages.  K only: the V half is neither filled nor reserved.
+template <int D, int F, bool kV, int kStages>
+struct QRing {
     using R = QRow<D, F>;
-    static constexpr int NT = NK / 8;  // 8-key tiles
+    static constexpr int RB = R::kBytes;
+    static constexpr int NK = RB <= 64 ? 32 : 16;        // keys of a stage
+    static constexpr int kKeyBytes = NK * RB, kHalf = kKeyBytes + NK * 4;
+    static constexpr int kStage = kHalf * (kV ? 2 : 1);  // codes, entries; K, then V
+    static constexpr int kBytes = kStages * (kStage + 16);
+    static constexpr int CH = RB / 16;                   // 16-byte chunks of a row
 
+    uint32_t base;  // shared address, 16-byte aligned
+
+    __device__ __forceinline__ uint32_t stage(int s) const { return base + (uint32_t)s * kStage; }
+    __device__ __forceinline__ uint32_t mask_at(int s) const {
+        return base + kStages * kStage + 16u * s;
+    }
+    __device__ static __forceinline__ uint32_t k_slot(int key, int c) {
+        const int n = (key & ~7) + 2 * (key & 3) + ((key >> 2) & 1);
+        return (uint32_t)(n * RB + ((RB == 128 ? c ^ (n & 1) : c) << 4));
+    }
+    __device__ static __forceinline__ uint32_t v_slot(int key, int c) {
+        const int x = RB == 128 ? (key & 3) << 1 : RB == 64 ? key & 2 : 0;
+        return (uint32_t)(key * RB + ((c ^ x) << 4));
+    }
+
+    // Starts the copies of the step whose first slot is slot0.  `mine`: row of
+    // slot slot0 + lane % NK, for sources that are not direct.
+    template <class Src>
+    __device__ __forceinline__ void fill(int s, const QuantCache& c, const Src& src, int slot0,
+                                         int mine) const {
+        const int lane = threadIdx.x & 31;
+        auto row = [&](int x) {
+            if constexpr (Src::kDirect) return src.row(slot0 + x);
+            else return __shfl_sync(0xffffffffu, mine, x);
+        };
+        const uint32_t st = stage(s);
+        constexpr int PER = 32 / CH;  // rows per pass of the warp
+        const int ch = lane % CH;
+#pragma unroll
+        for (int i = 0; i < NK / PER; ++i) {
+            const int key = lane / CH + i * PER;
+            const int r = row(key);
+            const size_t off = r >= 0 ? (size_t)r * RB + ch * 16 : 0;
+            cp_async16(st + k_slot(key, ch), c.kc + off, r >= 0);
+            if constexpr (kV) cp_async16(st + kHalf + v_slot(key, ch), c.vc + off, r >= 0);
+        }
+        if (lane < NK) {
+            int r;
+            if constexpr (Src::kDirect) r = src.row(slot0 + lane);
+            else r = mine;
+            const uint32_t at = st + kKeyBytes + 4u * ((lane & ~15) + 4 * (lane & 3) + ((lane >> 2) & 3));
+            const size_t off = r >= 0 ? (size_t)r : 0;
+            cp_async4(at, c.ks + off, r >= 0);
+            if constexpr (kV) cp_async4(at + kHalf, c.vs + off, r >= 0);
+        }
+        if constexpr (!Src::kDirect) {
+            const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
+            if (lane == 0)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(mask_at(s)), "r"(live) : "memory");
+        }
+    }
+    __device__ static __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+        const int n = valid ? 4 : 0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n));
+    }
+
+    // Bit x: slot slot0 + x counts (x < NK).
+    template <class Src>
+    __device__ __forceinline__ uint32_t live(int s, const Src& src, int slot0) const {
+        constexpr uint32_t kAll = NK == 32 ? 0xffffffffu : 0xffffu;
+        if constexpr (Src::kDirect) {
+            const int left = src.n - slot0;
+            return left >= NK ? kAll : (1u << max(left, 0)) - 1u;
+        } else {
+            uint32_t m;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(mask_at(s)) : "memory");
+            return m & kAll;
+        }
+    }
+
+    template <int N>
+    __device__ static __forceinline__ void lds(uint32_t (&w)[N], uint32_t a) {
+        if constexpr (N == 1)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a) : "memory");
+        else if constexpr (N == 2)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+        else
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(a)
+                         : "memory");
+    }
+    // Lane's quarter of the K row in column gid of tile j (all the stage's tiles).
+    __device__ __forceinline__ void k_words(uint32_t (&w)[R::kKW], int s, int j) const {
+        const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
+        const uint32_t a = stage(s) + (uint32_t)((8 * j + gid) * RB);
+        if constexpr (R::kKW == 8) {
+            uint32_t lo[4], hi[4];
+            lds<4>(lo, a + (((2 * t) ^ (gid & 1)) << 4));
+            lds<4>(hi, a + (((2 * t + 1) ^ (gid & 1)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = lo[i];
+                w[4 + i] = hi[i];
+            }
+        } else {
+            lds<R::kKW>(w, a + t * (RB / 4));
+        }
+    }
+    // Lane's eighth of the V row of key `key` (key % 4 == t).
+    __device__ __forceinline__ void v_words(uint32_t (&w)[R::kVW], int s, int key) const {
+        const int gid = (threadIdx.x & 31) >> 2;
+        constexpr int PER = 16 / (RB / 8);  // eighths per chunk: 4, 2 or 1
+        lds<R::kVW>(w, stage(s) + kHalf + v_slot(key, gid / PER) + (gid % PER) * (RB / 8));
+    }
+    // Entries of keys t, t + 4, t + 8, t + 12 of 16-key group i.
+    __device__ __forceinline__ void entries(uint32_t (&e)[4], int s, int i, bool v) const {
+        lds<4>(e, stage(s) + (v ? kHalf : 0) + kKeyBytes + 64u * i + 16u * (threadIdx.x & 3));
+    }
+};
+
+// ---------------------------------------------------------------- attention
+// A warp's query: 16 heads of a unit.
+template <int D, int F>
+struct QQuery {
     uint32_t qf[D / 16][4];
-    float qsum[2];       // sum of q, heads gid and gid + 8
-    float o[D / 8][4];   // tile j, element e: head gid + 8 (e / 2), dim (2t + e % 2) D / 8 + j
-    float m[2], l[2], zacc[2];
-
-    struct Regs {
-        uint32_t k[NT][R::kKW], v[NT][2][R::kVW], ks[NT][2], vs[NT][2];
-        uint32_t live;  // bit 2j + e: key 8j + 2t + e counts
-    };
+    float qsum[2];  // sum of the scaled q, heads gid and gid + 8
+    float kf[2];    // logit of the scaled q -> log2 domain
 
     // q: the unit's query rows, `stride` elements apart; rows g..15 are zero.
-    __device__ __forceinline__ void init(const __nv_bfloat16* q, size_t stride, int g) {
+    __device__ __forceinline__ void init(const __nv_bfloat16* q, size_t stride, int g,
+                                         float scale_log2) {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-        qsum[0] = qsum[1] = 0.f;
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
             const bool ok = gid + 8 * hr < g;
-            __nv_bfloat16 x[D / 4];
+            float x[D / 4], amax = 0.f;
             const uint4* src =
                 reinterpret_cast<const uint4*>(q + (size_t)(gid + 8 * hr) * stride + t * (D / 4));
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                reinterpret_cast<uint4*>(x)[i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) qsum[hr] += __bfloat162float(x[i]);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const __nv_bfloat162 pr =
-                        __halves2bfloat162(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
-                    qf[ks][2 * e + hr] = *reinterpret_cast<const uint32_t*>(&pr);
+                for (int e = 0; e < 4; ++e) {
+                    x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+                    x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^(14 - exponent); the exponent is held above -100, where q still fits
+            const int ex = max((int)(__float_as_uint(amax) >> 23), 27) - 127;
+            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            kf[hr] = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
+            qsum[hr] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) {
+                x[i] *= up;
+                qsum[hr] += x[i];
+            }
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    qf[ks][2 * e + hr] = pack_f16(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
             qsum[hr] += __shfl_xor_sync(0xffffffffu, qsum[hr], 1);
             qsum[hr] += __shfl_xor_sync(0xffffffffu, qsum[hr], 2);
+        }
+    }
+
+    // Logits, before kf, of the stage's keys: x[4 i + 2 j + e][hr] of key
+    // 16 i + t + 4 e + 8 j and head gid + 8 hr; -inf where `live` is clear.
+    template <class Ring>
+    __device__ __forceinline__ void logits(float (&x)[Ring::NK / 4][2], const Ring& ring, int s,
+                                           uint32_t live) const {
+        constexpr int NT = Ring::NK / 8;
+        float acc[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+            uint32_t w[Ring::R::kKW];
+            ring.k_words(w, s, j);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t b0, b1;
+                k_frag<F>(w, ks, b0, b1);
+                mma_f16(acc[j], qf[ks], b0, b1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+            uint32_t ent[4];
+            ring.entries(ent, s, i, false);
+#pragma unroll
+            for (int je = 0; je < 4; ++je) {
+                const float sc = entry_scale(ent[je]);
+                float z = entry_zero(ent[je]);
+                if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr)
+                    x[4 * i + je][hr] =
+                        fmaf(acc[2 * i + (je >> 1)][2 * hr + (je & 1)], sc, qsum[hr] * z);
+            }
+        }
+        if (live != (Ring::NK == 32 ? 0xffffffffu : 0xffffu)) {
+            const int t = threadIdx.x & 3;
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+                for (int je = 0; je < 4; ++je)
+                    if (!((live >> (16 * i + t + 4 * (je & 1) + 8 * (je >> 1))) & 1u))
+                        x[4 * i + je][0] = x[4 * i + je][1] = -INFINITY;
+        }
+    }
+};
+
+struct NoMaxima {
+    __device__ __forceinline__ void operator()(int, float, float) const {}
+};
+
+template <int D, int F, int kStages>
+struct QAttend {
+    using Ring = QRing<D, F, true, kStages>;
+    static constexpr int NK = Ring::NK, NT = NK / 8;
+
+    QQuery<D, F> q;
+    float o[D / 8][4];  // tile j, element e: head gid + 8 (e / 2), dim (2t + e % 2) D / 8 + j
+    float m[2], l[2], zacc[2];  // p = 2^(logit - m); m lies 10..14 below the running maximum
+    float up;                   // power of two above every |scale| seen: O counts in it
+
+    __device__ __forceinline__ void init(const __nv_bfloat16* qp, size_t stride, int g,
+                                         float scale_log2) {
+        q.init(qp, stride, g, scale_log2);
+        up = 0.f;
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
             m[hr] = -INFINITY;
             l[hr] = zacc[hr] = 0.f;
         }
@@ -225,153 +433,133 @@ struct QAttend {
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     }
 
-    // Issues the loads of one step.  `mine`: row of slot (step's first + lane),
-    // for sources that are not direct.
-    template <class Src>
-    __device__ __forceinline__ static void load(Regs& r, const QuantCache& c, const Src& src,
-                                                int slot0, int mine) {
-        const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-        auto row = [&](int x) {
-            if constexpr (Src::kDirect) return src.row(slot0 + x);
-            else return __shfl_sync(0xffffffffu, mine, x);
-        };
-        r.live = 0u;
+    // Moves the references to the step's maxima (log2 domain) and largest |scale|.
+    __device__ __forceinline__ void rescale(float mx0, float mx1, float sc) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int rk = row(8 * j + gid);
-            ldg_words<R::kKW>(r.k[j], c.kc + (size_t)rk * R::kBytes + t * (R::kBytes / 4), rk >= 0);
+        for (int w = 1; w < 32; w <<= 1) sc = fmaxf(sc, __shfl_xor_sync(0xffffffffu, sc, w));
+        float fo = 1.f;
+        if (sc > up) {
+            // 2^(exponent + 1), between 2^-125 and 2^126
+            const uint32_t ex = min(max(__float_as_uint(sc) >> 23, 1u) + 1u, 253u);
+            const float nu = __uint_as_float(ex << 23);
+            fo = up / nu;
+            up = nu;
         }
+        const float mx[2] = {mx0, mx1};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int hr = 0; hr < 2; ++hr) {
+            const float mn = fmaxf(m[hr], mx[hr] - 10.f);
+            const float f = mn == -INFINITY ? 1.f : exp2f(m[hr] - mn);
+            m[hr] = mn;
+            l[hr] *= f;
+            zacc[hr] *= f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rv = row(8 * j + 2 * t + e);
-                r.ks[j][e] = rv >= 0 ? __ldg(c.ks + rv) : 0u;
-                r.vs[j][e] = rv >= 0 ? __ldg(c.vs + rv) : 0u;
-                ldg_words<R::kVW>(r.v[j][e], c.vc + (size_t)rv * R::kBytes + gid * (R::kBytes / 8),
-                                  rv >= 0);
-                if (rv >= 0) r.live |= 1u << (2 * j + e);
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][2 * hr] *= f * fo;
+                o[j][2 * hr + 1] *= f * fo;
             }
         }
     }
 
-    __device__ __forceinline__ void step(const Regs& r, float scale_log2) {
-        float s[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t b0, b1;
-                k_frag<F>(r.k[j], ks, b0, b1);
-                mma_bf16(s[j], qf[ks], b0, b1);
-            }
-        }
-        // logits in the log2 domain; masked keys -inf
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float sc = entry_scale(r.ks[j][e]);
-                float z = entry_zero(r.ks[j][e]);
-                if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
-                const float s2 = sc * scale_log2, z2 = z * scale_log2;
-                const bool ok = (r.live >> (2 * j + e)) & 1u;
-#pragma unroll
-                for (int hr = 0; hr < 2; ++hr) {
-                    float& x = s[j][2 * hr + e];
-                    x = ok ? fmaf(x, s2, qsum[hr] * z2) : -INFINITY;
-                    mx[hr] = fmaxf(mx[hr], x);
-                }
-            }
-        }
-        // the reference may lag the maximum by up to 2^8 before O is rescaled
-        bool grow = false;
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
-            grow |= mx[hr] > m[hr] + 8.f;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-                const float mn = fmaxf(m[hr], mx[hr]);
-                const float f = mn == -INFINITY ? 1.f : exp2f(m[hr] - mn);
-                m[hr] = mn;
-                l[hr] *= f;
-                zacc[hr] *= f;
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][2 * hr] *= f;
-                    o[j][2 * hr + 1] *= f;
-                }
-            }
-        }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    // One stage's keys.  maxima(step, head gid's, head gid + 8's): the step's
+    // largest logit per head, log2 domain, the same in a quad.
+    template <class Maxima>
+    __device__ __forceinline__ void step(const Ring& ring, int s, uint32_t live, int at,
+                                         const Maxima& maxima) {
+        float x[NK / 4][2];
+        q.logits(x, ring, s, live);
+        uint32_t ent[NT / 2][4];
+        float mx[2], big = 0.f;
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
-            uint32_t a[4];
+            ring.entries(ent[i], s, i, true);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int j = 2 * i + jj;
-                float w[4];
+            for (int je = 0; je < 4; ++je) big = fmaxf(big, fabsf(entry_scale(ent[i][je])));
+        }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float sc = entry_scale(r.vs[j][e]);
-                    float z = entry_zero(r.vs[j][e]);
-                    if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
+        for (int hr = 0; hr < 2; ++hr) {
+            mx[hr] = x[0][hr];
 #pragma unroll
-                    for (int hr = 0; hr < 2; ++hr) {
-                        const float p = exp2f(s[j][2 * hr + e] - mu[hr]);
-                        l[hr] += p;
-                        zacc[hr] = fmaf(p, z, zacc[hr]);
-                        w[2 * hr + e] = p * sc;
-                    }
+            for (int i = 1; i < NK / 4; ++i) mx[hr] = fmaxf(mx[hr], x[i][hr]);
+            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
+            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
+            mx[hr] *= q.kf[hr];
+        }
+        maxima(at, mx[0], mx[1]);
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + 14.f || mx[1] > m[1] + 14.f || big > up))
+            rescale(mx[0], mx[1], big);
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        const float down = up == 0.f ? 0.f : __uint_as_float(0x7f000000u - __float_as_uint(up));
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+            float w[4][2];
+#pragma unroll
+            for (int je = 0; je < 4; ++je) {
+                const float sc = entry_scale(ent[i][je]);
+                float z = entry_zero(ent[i][je]);
+                if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
+                const float sd = sc * down;
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr) {
+                    const float p = exp2_approx(fmaf(x[4 * i + je][hr], q.kf[hr], -mu[hr]));
+                    l[hr] += p;
+                    zacc[hr] = fmaf(p, z, zacc[hr]);
+                    w[je][hr] = p * sd;
                 }
-                a[2 * jj] = pack_bf16(w[0], w[1]);
-                a[2 * jj + 1] = pack_bf16(w[2], w[3]);
             }
+            const uint32_t a[4] = {pack_f16(w[0][0], w[1][0]), pack_f16(w[0][1], w[1][1]),
+                                   pack_f16(w[2][0], w[3][0]), pack_f16(w[2][1], w[3][1])};
+            uint32_t v[4][Ring::R::kVW];
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                const uint32_t b0 = v_pair<F>(r.v[2 * i][0], r.v[2 * i][1], j);
-                const uint32_t b1 = v_pair<F>(r.v[2 * i + 1][0], r.v[2 * i + 1][1], j);
-                mma_bf16(o[j], a, b0, b1);
+            for (int je = 0; je < 4; ++je) ring.v_words(v[je], s, 16 * i + (threadIdx.x & 3) + 4 * je);
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 2) {
+                uint32_t b0[2], b1[2];
+                v_pairs<F>(v[0], v[1], j, b0[0], b0[1]);
+                v_pairs<F>(v[2], v[3], j, b1[0], b1[1]);
+                mma_f16(o[j], a, b0[0], b1[0]);
+                mma_f16(o[j + 1], a, b0[1], b1[1]);
             }
         }
     }
 
     // Steps first, first + stride, ... below n_steps of a source's list.
-    template <class Src>
-    __device__ __forceinline__ void run(const QuantCache& c, const Src& src, int first, int stride,
-                                        int n_steps, float scale_log2) {
-        if (first >= n_steps) return;
+    template <class Src, class Maxima>
+    __device__ __forceinline__ void run(const Ring& ring, const QuantCache& c, const Src& src,
+                                        int first, int stride, int n_steps, const Maxima& maxima) {
         const int lane = threadIdx.x & 31;
         auto mine = [&](int st) {
             if constexpr (Src::kDirect) return 0;
             else return st < n_steps ? src.row(st * NK + (lane & (NK - 1))) : -1;
         };
-        // one step ahead in registers, and the rows' places two ahead
-        Regs a, b;
-        load(a, c, src, first * NK, mine(first));
-        int row = mine(first + stride);
-        for (int st = first;;) {
-            st += stride;
-            if (st < n_steps) load(b, c, src, st * NK, row);
-            row = mine(st + stride);
-            step(a, scale_log2);
-            if (st >= n_steps) break;
-            st += stride;
-            if (st < n_steps) load(a, c, src, st * NK, row);
-            row = mine(st + stride);
-            step(b, scale_log2);
-            if (st >= n_steps) break;
+        // copies run kStages - 1 steps ahead, the rows' places one more
+        int ahead = first;
+        int row = mine(first);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (ahead < n_steps) ring.fill(i, c, src, ahead * NK, row);
+            cp_async_commit();
+            ahead += stride;
+            row = mine(ahead);
         }
+        int s = 0, fs = kStages - 1;
+        for (int st = first; st < n_steps; st += stride) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            if (ahead < n_steps) ring.fill(fs, c, src, ahead * NK, row);
+            cp_async_commit();
+            ahead += stride;
+            row = mine(ahead);
+            step(ring, s, ring.live(s, src, st * NK), st, maxima);
+            s = s + 1 == kStages ? 0 : s + 1;
+            fs = fs + 1 == kStages ? 0 : fs + 1;
+        }
+        cp_async_wait<0>();
+        __syncwarp();  // the ring may be reused
     }
 
-    // Sums over the quad and adds the zero points: o = sum p v^, l = sum p.
+    // Sums over the quad, puts O in its own units and adds the zero points:
+    // o = sum p v^, l = sum p.
     __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
@@ -381,14 +569,14 @@ struct QAttend {
             zacc[hr] += __shfl_xor_sync(0xffffffffu, zacc[hr], 2);
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
-                o[j][2 * hr] += zacc[hr];
-                o[j][2 * hr + 1] += zacc[hr];
+                o[j][2 * hr] = fmaf(o[j][2 * hr], up, zacc[hr]);
+                o[j][2 * hr + 1] = fmaf(o[j][2 * hr + 1], up, zacc[hr]);
             }
         }
     }
 
-    // Partial (after finish): part[h] = {m, l}, then O rows of D floats at
-    // part + 32 (16 heads).
+    // Partial (after finish): part[2 h] = m, part[2 h + 1] = l, then O rows of D
+    // floats at part + 32 (16 heads).
     __device__ __forceinline__ void store_part(float* part, int g) const {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
 #pragma unroll

@@ -14,8 +14,10 @@ namespace hs {
 namespace sq {
 
 constexpr int kWarps = 4;
-// Keys of a step: 32 4-bit rows or 16 8-bit ones fill the same registers.
-template <int F> constexpr int kStep = F == HS_KV_INT4 ? 32 : 16;
+constexpr int kStages = 3;
+template <int D, int F> using Attend = QAttend<D, F, kStages>;
+template <int D, int F>
+constexpr size_t kRingBytes = (size_t)kWarps * Attend<D, F>::Ring::kBytes;
 
 // Writes a unit's heads from a warp's finished accumulators.
 template <int D, class A>
@@ -45,7 +47,7 @@ __device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o,
 }
 
 template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                         const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
                         __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
@@ -55,13 +57,15 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int unit = (int)(task / p.t_q);
     const int u = unit % p.hkv, b = unit / p.hkv;
     const size_t head0 = ((size_t)b * p.hq + (size_t)u * p.group) * p.t_q + j;
-    QAttend<D, F, kStep<F>> st;
-    st.init(q + head0 * D, (size_t)p.t_q * D, p.group);
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    using A = Attend<D, F>;
+    const typename A::Ring ring{smem_u32(smem_raw) + (threadIdx.x >> 5) * A::Ring::kBytes};
+    A st;
+    st.init(q + head0 * D, (size_t)p.t_q * D, p.group, p.scale_log2);
     const int n = clamp_count(cnt[task], p.ksel) * p.block_size;
     const QIndex src{idx + (size_t)task * p.ksel, n,           p.block_size,
                      p.q_offset + j,              p.bt != nullptr, page_map(p, b, u)};
-    const int steps = (n + kStep<F> - 1) / kStep<F>;
-    st.run(unit_cache<D, F>(p, cache, unit), src, 0, 1, steps, p.scale_log2);
+    st.run(ring, unit_cache<D, F>(p, cache, unit), src, 0, 1, (n + A::NK - 1) / A::NK, NoMaxima{});
     st.finish();
     store_rows<D>(st, p.group, o, lse, head0, (size_t)p.t_q);
 }
@@ -72,14 +76,18 @@ __device__ __forceinline__ float merge_weight(float m, float M) {
 }
 
 template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     decode_sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                                const int32_t* __restrict__ seq_len,
                                const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
                                int csize, __nv_bfloat16* __restrict__ o,
                                float* __restrict__ lse) {
-    using A = QAttend<D, F, kStep<F>>;
-    extern __shared__ __align__(16) float smem[];  // kWarps + 1 partials
+    using A = Attend<D, F>;
+    // the warps' rings, reused for their partials; then the CTA's partial
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    constexpr int kStride = A::Ring::kBytes / 4;  // floats between the warps' partials
+    static_assert(kStride >= A::kPart, "a partial fits a ring");
+    float* smem = reinterpret_cast<float*>(smem_raw);
     const int warp = threadIdx.x >> 5, g = p.group;
     const int crank = csize > 1 ? (int)cluster_rank() : 0;
     const int unit = blockIdx.x / csize;
@@ -88,31 +96,32 @@ __global__ void __launch_bounds__(kWarps * 32)
     const bool valid = L >= 1 && L <= p.t_kv;
     const size_t head0 = (size_t)b * p.hq + (size_t)u * g;
     A st;
-    st.init(q + head0 * D, D, g);
+    st.init(q + head0 * D, D, g, p.scale_log2);
+    const typename A::Ring ring{smem_u32(smem_raw) + warp * A::Ring::kBytes};
     if (valid) {
         const int n = clamp_count(cnt[unit], p.ksel);
         const QIndex src{idx + (size_t)unit * p.ksel, n, 1, L - 1, p.bt != nullptr,
                          page_map(p, b, u)};
-        st.run(unit_cache<D, F>(p, cache, unit), src, crank * kWarps + warp, kWarps * csize,
-               (n + kStep<F> - 1) / kStep<F>, p.scale_log2);
+        st.run(ring, unit_cache<D, F>(p, cache, unit), src, crank * kWarps + warp, kWarps * csize,
+               (n + A::NK - 1) / A::NK, NoMaxima{});
     } else if (crank == 0 && threadIdx.x == 0) {
         set_status(HS_ERR_BOUNDS);
     }
     st.finish();
-    st.store_part(smem + warp * A::kPart, g);
+    st.store_part(smem + warp * kStride, g);
     __syncthreads();
     // the CTA's partial
-    float* mine = smem + kWarps * A::kPart;
+    float* mine = smem + kWarps * kStride;
     for (int e = threadIdx.x; e < g * D; e += blockDim.x) {
         const int h = e / D;
         float M = -INFINITY, l = 0.f, acc = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * A::kPart + 2 * h]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * kStride + 2 * h]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = merge_weight(smem[w * A::kPart + 2 * h], M);
-            l += smem[w * A::kPart + 2 * h + 1] * f;
-            acc += smem[w * A::kPart + 32 + e] * f;
+            const float f = merge_weight(smem[w * kStride + 2 * h], M);
+            l += smem[w * kStride + 2 * h + 1] * f;
+            acc += smem[w * kStride + 32 + e] * f;
         }
         mine[32 + e] = acc;
         if (e % D == 0) {
@@ -147,7 +156,11 @@ static cudaError_t launch_sparse_t(const KParams& p, const QuantCache& c, const 
                                    const int32_t* idx, const int32_t* cnt, void* o, float* lse,
                                    cudaStream_t st) {
     const long long tasks = (long long)p.batch * p.hkv * p.t_q;
-    sparse_quant_kernel<D, F><<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(
+    auto kern = sparse_quant_kernel<D, F>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)kRingBytes<D, F>);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, kRingBytes<D, F>, st>>>(
         p, c, (const __nv_bfloat16*)q, idx, cnt, (__nv_bfloat16*)o, lse);
     return cudaGetLastError();
 }
@@ -157,7 +170,7 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
                                    const int32_t* seq_len, const int32_t* idx, const int32_t* cnt,
                                    void* o, float* lse, cudaStream_t st) {
     auto kern = decode_sparse_quant_kernel<D, F>;
-    const size_t smem = (kWarps + 1) * QAttend<D, F, kStep<F>>::kPart * sizeof(float);
+    const size_t smem = kRingBytes<D, F> + Attend<D, F>::kPart * sizeof(float);
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -168,7 +181,7 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
     // Widest cluster (a portable size) whose CTAs still run in one wave, two
     // to an SM, with a step for every warp.
     const int units = p.batch * p.hkv;
-    const int steps = (p.ksel + kStep<F> - 1) / kStep<F>;
+    const int steps = (p.ksel + Attend<D, F>::NK - 1) / Attend<D, F>::NK;
     int csize = 1;
     while (csize < 8 && units * csize * 2 <= 2 * sms && kWarps * csize < steps) csize *= 2;
     cudaLaunchConfig_t cfg = {};
