@@ -356,8 +356,8 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&
         row = mine(ahead);
         if (st < n_steps) {
             const uint32_t live = ring.live(s, src, st * NK);
-            float x[NK / 4][2];
-            q.logits(x, ring, s, live);
+            float2 x[NK / 8][2];
+            q.logits(x, ring, ring.stage(s), live);
 #pragma unroll
             for (int i = 0; i < NK / 16; ++i) {
                 // v[je]: key t + 4 je of the group, this lane's two heads; then the
@@ -365,9 +365,10 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&
                 float v[4];
 #pragma unroll
                 for (int je = 0; je < 4; ++je) {
-                    const float(&y)[2] = x[4 * i + je];
-                    v[je] = fmaxf(fmaxf(-INFINITY, __fsub_rn(__fmul_rn(y[0], q.kf[0]), lse2[0])),
-                                  __fsub_rn(__fmul_rn(y[1], q.kf[1]), lse2[1]));
+                    const float2(&y)[2] = x[2 * i + (je >> 1)];
+                    const float y0 = je & 1 ? y[0].y : y[0].x, y1 = je & 1 ? y[1].y : y[1].x;
+                    v[je] = fmaxf(fmaxf(-INFINITY, __fsub_rn(__fmul_rn(y0, q.kf[0]), lse2[0])),
+                                  __fsub_rn(__fmul_rn(y1, q.kf[1]), lse2[1]));
                 }
                 const bool up = lane & 16, up2 = lane & 8;
                 const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);

@@ -7,16 +7,14 @@
 // e4m3 number, one byte per element.
 //
 // Attention never rebuilds the values.  For a key with entry (s, z),
-//     scale q.k^ = scale (s (q.c') + z' sum(q)),
-//     sum_i p_i v^_i = sum_i (p_i s_i) c'_i + sum_i p_i z'_i,
-// with c' = c - 8, z' = z + 8 s in 4 bits and c' = c, z' = z in 8.  c' is exact in
-// fp16, so both products run on codes in fp16 MMAs with fp32 accumulators, and
-// scale and zero are applied to the logits, to P and to one running sum per
-// head.  fp16 rather than bf16: two of a half-word's four nibbles turn into
-// fp16 without a shift, and e4m3 has a conversion instruction; integer and
-// logic instructions issue every other cycle and were what bounded a bf16
-// form of this (33% of issue slots, half of them on that pipe).  What fp16's
-// range needs:
+//     scale q.k^ = scale (s (q.c) + z sum(q)),
+//     sum_i p_i v^_i = sum_i (p_i s_i) c_i + sum_i p_i z_i:
+// both products run on the codes, exact in fp16, with fp32 accumulators
+// (mma.m16n8k16), and scale and zero are applied to the logits, to P and to one
+// running sum per head.  fp16 rather than bf16, because codes reach it in few
+// instructions: a 4-bit code in a byte, read as e4m3, is the number c 2^-9,
+// exactly, for all of 0..15 (subnormals, then the first binade), so both formats use
+// the conversion of e4m3 pairs.  What fp16's range needs:
 //  - q is scaled by a power of two per head so that max|q| lies in [2^14, 2^15);
 //    a bf16 element is then exact unless it is 2^-29 of the largest or less
 //    (error 2^-39 of the largest);
@@ -24,7 +22,10 @@
 //    2^14 before O is rescaled) and to a power of two above the largest |s_i|
 //    seen, and rounded to fp16: relative 2^-12 for weights down to 2^-24 of the
 //    largest, an absolute 2^-35 of it below.
-// Everything else is fp32.
+// Everything else is fp32.  What bounds the kernels is the issue rate: mma.sync
+// holds its scheduler for 8 cycles (measured alone 8.7 cycles, with 4 FFMAs beside it
+// 12.8, with 8 of them 17), so 16 keys of 128 dims take 256 issue cycles for their
+// 32 MMAs beside some 250 for unpacking, the softmax and the reads.
 //
 // One warp, 16 heads as the rows of mma.m16n8k16, 16 keys at a time.  Lane
 // (gid, t) of the warp (gid = lane / 4, t = lane % 4) needs of a key's K row the
@@ -37,10 +38,12 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "attend_mma.cuh"
 #include "hs_common.cuh"
 #include "hs_kernels.cuh"
+#include "tc_ptx.cuh"
 
 namespace hs {
 
@@ -80,61 +83,45 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+// The e4m3 pairs in the low and in the high half of x as fp16 pairs (exact).
+__device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
 
-// The 4-bit codes in bits 0..3 (nibble 0) or 4..7 (nibble 1) of x's halves, as an
-// fp16 pair c - 8: 0x6400 | c is the fp16 number 1024 + c, 0x6400 | 16 c is
-// 1024 + 16 c, and both steps back are exact.
-template <int NIBBLE>
-__device__ __forceinline__ uint32_t int4_pair(uint32_t x) {
-    if constexpr (NIBBLE == 0)
-        return as_u32(__hsub2(as_half2((x & 0x000f000fu) | 0x64006400u), as_half2(0x64086408u)));
-    else
-        return as_u32(__hfma2(as_half2((x & 0x00f000f0u) | 0x64006400u), as_half2(0x2c002c00u),
-                              as_half2(0xd480d480u)));
-}
-// The two e4m3 codes in the low half of x as an fp16 pair (exact).
-__device__ __forceinline__ uint32_t fp8_pair(uint32_t x) {
-    uint32_t r;
-    asm("{.reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
-    return r;
-}
+// What a code of 1 counts for in the operands.
+template <int F> constexpr float kCodeUnit = F == HS_KV_INT4 ? 1.f / 512.f : 1.f;
 
 // Dimension (of a quarter row) that element e (0: b0 low, 1: b0 high, 2: b1
 // low, 3: b1 high) of k step `ks` holds.
 template <int F>
 __host__ __device__ constexpr int k_dim(int ks, int e) {
-    return F == HS_KV_INT4 ? 8 * (ks >> 1) + 2 * (ks & 1) + (e >> 1) + 4 * (e & 1) : 4 * ks + e;
+    return F == HS_KV_INT4 ? 8 * (ks >> 1) + (ks & 1) + 2 * e : 4 * ks + e;
 }
 
 // B fragment (b0, b1) of k step `ks` from a lane's quarter of a K row.
 template <int F, int N>
 __device__ __forceinline__ void k_frag(const uint32_t (&w)[N], int ks, uint32_t& b0, uint32_t& b1) {
-    if constexpr (F == HS_KV_INT4) {
-        const uint32_t x = w[ks >> 1] >> (8 * (ks & 1));
-        b0 = int4_pair<0>(x);
-        b1 = int4_pair<1>(x);
-    } else {
-        b0 = fp8_pair(w[ks]);
-        b1 = fp8_pair(w[ks] >> 16);
-    }
+    if constexpr (F == HS_KV_INT4)
+        e4m3_f16((ks & 1 ? w[ks >> 1] >> 4 : w[ks >> 1]) & 0x0f0f0f0fu, b0, b1);
+    else
+        e4m3_f16(w[ks], b0, b1);
 }
 
-// Pairs (a[j], b[j]) and (a[j + 1], b[j + 1]) of a lane's eighths of two V rows,
-// j even.
+// Pairs (a[j + i], b[j + i]), i = 0..3, of a lane's eighths of two V rows, j a
+// multiple of 4.
 template <int F, int N>
 __device__ __forceinline__ void v_pairs(const uint32_t (&a)[N], const uint32_t (&b)[N], int j,
-                                        uint32_t& p0, uint32_t& p1) {
+                                        uint32_t (&p)[4]) {
     if constexpr (F == HS_KV_INT4) {
-        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7632 : 0x5410) >>
-                           (4 * (j & 2));
-        p0 = int4_pair<0>(x);
-        p1 = int4_pair<1>(x);
+        // bytes (a, b, a, b) of two neighbouring bytes of each row
+        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7362 : 0x5140);
+        e4m3_f16(x & 0x0f0f0f0fu, p[0], p[2]);
+        e4m3_f16((x >> 4) & 0x0f0f0f0fu, p[1], p[3]);
     } else {
-        const uint32_t x = __byte_perm(a[j >> 2], b[j >> 2], (j & 2) ? 0x7362 : 0x5140);
-        p0 = fp8_pair(x);
-        p1 = fp8_pair(x >> 16);
+        e4m3_f16(__byte_perm(a[j >> 2], b[j >> 2], 0x5140), p[0], p[1]);
+        e4m3_f16(__byte_perm(a[j >> 2], b[j >> 2], 0x7362), p[2], p[3]);
     }
 }
 
@@ -195,7 +182,20 @@ struct QRing {
     static constexpr int CH = RB / 16;                   // 16-byte chunks of a row
 
     uint32_t base;  // shared address, 16-byte aligned
+    // the lane's places in a stage: what it reads, and where its copies go
+    uint32_t k_at, v_at, e_at, k_to, v_to, e_to;
 
+    __device__ __forceinline__ explicit QRing(uint32_t at) : base(at) {
+        const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
+        const int row = lane / CH, ch = lane % CH;
+        constexpr int PER = 16 / (RB / 8) > 0 ? 16 / (RB / 8) : 1;  // eighths per chunk
+        k_at = (uint32_t)(gid * RB + (RB == 128 ? ((2 * t) ^ (gid & 1)) << 4 : t * (RB / 4)));
+        v_at = (uint32_t)(kHalf + v_slot(t, gid / PER) + (gid % PER) * (RB / 8));
+        e_at = (uint32_t)(kKeyBytes + 16 * t);
+        k_to = k_slot(row, ch);
+        v_to = kHalf + v_slot(row, ch);
+        e_to = (uint32_t)(kKeyBytes + 4 * ((lane & ~15) + 4 * (lane & 3) + ((lane >> 2) & 3)));
+    }
     __device__ __forceinline__ uint32_t stage(int s) const { return base + (uint32_t)s * kStage; }
     __device__ __forceinline__ uint32_t mask_at(int s) const {
         return base + kStages * kStage + 16u * s;
@@ -208,6 +208,13 @@ struct QRing {
         const int x = RB == 128 ? (key & 3) << 1 : RB == 64 ? key & 2 : 0;
         return (uint32_t)(key * RB + ((c ^ x) << 4));
     }
+    // K place of row lane / CH + i * PASS, from that of row lane / CH: PASS rows are
+    // 512 bytes; of 128-byte rows, 4 of them are half a tile, whose rows are the odd ones.
+    static constexpr int PASS = 32 / CH;
+    __device__ __forceinline__ uint32_t k_dst(int i) const {
+        if constexpr (RB == 128) return (i & 1 ? (k_to ^ 16u) + 128u : k_to) + (uint32_t)(i >> 1) * 1024u;
+        else return k_to + (uint32_t)i * 512u;
+    }
 
     // Starts the copies of the step whose first slot is slot0.  `mine`: row of
     // slot slot0 + lane % NK, for sources that are not direct.
@@ -215,35 +222,62 @@ struct QRing {
     __device__ __forceinline__ void fill(int s, const QuantCache& c, const Src& src, int slot0,
                                          int mine) const {
         const int lane = threadIdx.x & 31;
-        auto row = [&](int x) {
-            if constexpr (Src::kDirect) return src.row(slot0 + x);
-            else return __shfl_sync(0xffffffffu, mine, x);
-        };
         const uint32_t st = stage(s);
-        constexpr int PER = 32 / CH;  // rows per pass of the warp
-        const int ch = lane % CH;
+        if constexpr (Src::kDirect) {
+            const int r0 = src.first + slot0;
+            if (slot0 + NK <= src.n) {  // a whole step: consecutive bytes
+                const uint8_t* kp = c.kc + (size_t)r0 * RB + lane * 16;
+                const uint8_t* vp = c.vc + (size_t)r0 * RB + lane * 16;
 #pragma unroll
-        for (int i = 0; i < NK / PER; ++i) {
-            const int key = lane / CH + i * PER;
-            const int r = row(key);
-            const size_t off = r >= 0 ? (size_t)r * RB + ch * 16 : 0;
-            cp_async16(st + k_slot(key, ch), c.kc + off, r >= 0);
-            if constexpr (kV) cp_async16(st + kHalf + v_slot(key, ch), c.vc + off, r >= 0);
+                for (int i = 0; i < NK / PASS; ++i) {
+                    copy16(st + k_dst(i), kp + i * 512);
+                    if constexpr (kV) copy16(st + v_to + i * 512, vp + i * 512);
+                }
+                if (NK == 32 || lane < NK) {
+                    copy4(st + e_to, c.ks + (size_t)r0 + lane);
+                    if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (size_t)r0 + lane);
+                }
+                return;
+            }
+            mine = src.row(slot0 + (lane & (NK - 1)));
         }
-        if (lane < NK) {
-            int r;
-            if constexpr (Src::kDirect) r = src.row(slot0 + lane);
-            else r = mine;
-            const uint32_t at = st + kKeyBytes + 4u * ((lane & ~15) + 4 * (lane & 3) + ((lane >> 2) & 3));
-            const size_t off = r >= 0 ? (size_t)r : 0;
-            cp_async4(at, c.ks + off, r >= 0);
-            if constexpr (kV) cp_async4(at + kHalf, c.vs + off, r >= 0);
+        const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
+        if (live == 0xffffffffu) {
+#pragma unroll
+            for (int i = 0; i < NK / PASS; ++i) {
+                const uint32_t r = __shfl_sync(0xffffffffu, mine, lane / CH + i * PASS);
+                const size_t off = (size_t)r * RB + (lane % CH) * 16;
+                copy16(st + k_dst(i), c.kc + off);
+                if constexpr (kV) copy16(st + v_to + i * 512, c.vc + off);
+            }
+            if (NK == 32 || lane < NK) {
+                copy4(st + e_to, c.ks + (uint32_t)mine);
+                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (uint32_t)mine);
+            }
+        } else {  // rows that do not count are zeros
+#pragma unroll
+            for (int i = 0; i < NK / PASS; ++i) {
+                const int r = __shfl_sync(0xffffffffu, mine, lane / CH + i * PASS);
+                const size_t off = r >= 0 ? (size_t)r * RB + (lane % CH) * 16 : 0;
+                cp_async16(st + k_dst(i), c.kc + off, r >= 0);
+                if constexpr (kV) cp_async16(st + v_to + i * 512, c.vc + off, r >= 0);
+            }
+            if (NK == 32 || lane < NK) {
+                const size_t off = mine >= 0 ? (size_t)mine : 0;
+                cp_async4(st + e_to, c.ks + off, mine >= 0);
+                if constexpr (kV) cp_async4(st + kHalf + e_to, c.vs + off, mine >= 0);
+            }
         }
         if constexpr (!Src::kDirect) {
-            const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
             if (lane == 0)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(mask_at(s)), "r"(live) : "memory");
         }
+    }
+    __device__ static __forceinline__ void copy16(uint32_t dst, const void* src) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+    }
+    __device__ static __forceinline__ void copy4(uint32_t dst, const void* src) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
     }
     __device__ static __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
         const int n = valid ? 4 : 0;
@@ -276,41 +310,55 @@ struct QRing {
                          : "r"(a)
                          : "memory");
     }
-    // Lane's quarter of the K row in column gid of tile j (all the stage's tiles).
-    __device__ __forceinline__ void k_words(uint32_t (&w)[R::kKW], int s, int j) const {
-        const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-        const uint32_t a = stage(s) + (uint32_t)((8 * j + gid) * RB);
+    // Lane's quarter of the K row in column gid of tile j.
+    __device__ __forceinline__ void k_words(uint32_t (&w)[R::kKW], uint32_t st, int j) const {
+        const uint32_t a = st + k_at + (uint32_t)(8 * j * RB);
         if constexpr (R::kKW == 8) {
             uint32_t lo[4], hi[4];
-            lds<4>(lo, a + (((2 * t) ^ (gid & 1)) << 4));
-            lds<4>(hi, a + (((2 * t + 1) ^ (gid & 1)) << 4));
+            lds<4>(lo, a);
+            lds<4>(hi, st + (k_at ^ 16u) + (uint32_t)(8 * j * RB));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 w[i] = lo[i];
                 w[4 + i] = hi[i];
             }
         } else {
-            lds<R::kKW>(w, a + t * (RB / 4));
+            lds<R::kKW>(w, a);
         }
     }
-    // Lane's eighth of the V row of key `key` (key % 4 == t).
-    __device__ __forceinline__ void v_words(uint32_t (&w)[R::kVW], int s, int key) const {
-        const int gid = (threadIdx.x & 31) >> 2;
-        constexpr int PER = 16 / (RB / 8);  // eighths per chunk: 4, 2 or 1
-        lds<R::kVW>(w, stage(s) + kHalf + v_slot(key, gid / PER) + (gid % PER) * (RB / 8));
+    // Lane's eighth of the V row of key 16 i + t + 4 je.
+    __device__ __forceinline__ void v_words(uint32_t (&w)[R::kVW], uint32_t st, int i, int je) const {
+        lds<R::kVW>(w, st + v_at + (uint32_t)((16 * i + 4 * je) * RB));
     }
     // Entries of keys t, t + 4, t + 8, t + 12 of 16-key group i.
-    __device__ __forceinline__ void entries(uint32_t (&e)[4], int s, int i, bool v) const {
-        lds<4>(e, stage(s) + (v ? kHalf : 0) + kKeyBytes + 64u * i + 16u * (threadIdx.x & 3));
+    __device__ __forceinline__ void entries(uint32_t (&e)[4], uint32_t st, int i, bool v) const {
+        lds<4>(e, st + e_at + (v ? kHalf : 0) + 64u * i);
     }
 };
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    uint64_t ra, rb, rd;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Scales and zero points of two entries.
+__device__ __forceinline__ void entry_pair(uint32_t e0, uint32_t e1, float2& sc, float2& z) {
+    sc = make_float2(entry_scale(e0), entry_scale(e1));
+    z = make_float2(entry_zero(e0), entry_zero(e1));
+}
 
 // ---------------------------------------------------------------- attention
 // A warp's query: 16 heads of a unit.
 template <int D, int F>
 struct QQuery {
     uint32_t qf[D / 16][4];
-    float qsum[2];  // sum of the scaled q, heads gid and gid + 8
+    float qsum[2];  // sum of the scaled q in units of the operands, heads gid and gid + 8
     float kf[2];    // logit of the scaled q -> log2 domain
 
     // q: the unit's query rows, `stride` elements apart; rows g..15 are zero.
@@ -340,28 +388,31 @@ struct QQuery {
             // 2^(14 - exponent); the exponent is held above -100, where q still fits
             const int ex = max((int)(__float_as_uint(amax) >> 23), 27) - 127;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            kf[hr] = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
-            qsum[hr] = 0.f;
+            kf[hr] = fmaxf(scale_log2 / kCodeUnit<F> *
+                               __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
+            float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) {
                 x[i] *= up;
-                qsum[hr] += x[i];
+                sum += x[i];
             }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            qsum[hr] = sum * kCodeUnit<F>;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     qf[ks][2 * e + hr] = pack_f16(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
-            qsum[hr] += __shfl_xor_sync(0xffffffffu, qsum[hr], 1);
-            qsum[hr] += __shfl_xor_sync(0xffffffffu, qsum[hr], 2);
         }
     }
 
-    // Logits, before kf, of the stage's keys: x[4 i + 2 j + e][hr] of key
-    // 16 i + t + 4 e + 8 j and head gid + 8 hr; -inf where `live` is clear.
+    // Logits, before kf, of the stage's keys: x[j][hr] of keys t + 8 j (.x) and t + 4
+    // + 8 j (.y) past each 16 (j even: the first 8 of them) and head gid + 8 hr; -inf
+    // where `live` is clear.
     template <class Ring>
-    __device__ __forceinline__ void logits(float (&x)[Ring::NK / 4][2], const Ring& ring, int s,
-                                           uint32_t live) const {
+    __device__ __forceinline__ void logits(float2 (&x)[Ring::NK / 8][2], const Ring& ring,
+                                           uint32_t st, uint32_t live) const {
         constexpr int NT = Ring::NK / 8;
         float acc[NT][4];
 #pragma unroll
@@ -369,7 +420,7 @@ struct QQuery {
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
             uint32_t w[Ring::R::kKW];
-            ring.k_words(w, s, j);
+            ring.k_words(w, st, j);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t b0, b1;
@@ -380,26 +431,25 @@ struct QQuery {
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
             uint32_t ent[4];
-            ring.entries(ent, s, i, false);
+            ring.entries(ent, st, i, false);
 #pragma unroll
-            for (int je = 0; je < 4; ++je) {
-                const float sc = entry_scale(ent[je]);
-                float z = entry_zero(ent[je]);
-                if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
+            for (int jj = 0; jj < 2; ++jj) {
+                float2 sc, z;
+                entry_pair(ent[2 * jj], ent[2 * jj + 1], sc, z);
+                const float* a = acc[2 * i + jj];
 #pragma unroll
                 for (int hr = 0; hr < 2; ++hr)
-                    x[4 * i + je][hr] =
-                        fmaf(acc[2 * i + (je >> 1)][2 * hr + (je & 1)], sc, qsum[hr] * z);
+                    x[2 * i + jj][hr] = tc::ffma2(make_float2(a[2 * hr], a[2 * hr + 1]), sc,
+                                                  fmul2(both(qsum[hr]), z));
             }
         }
         if (live != (Ring::NK == 32 ? 0xffffffffu : 0xffffu)) {
-            const int t = threadIdx.x & 3;
+            const uint32_t mine = live >> (threadIdx.x & 3);
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i)
-#pragma unroll
-                for (int je = 0; je < 4; ++je)
-                    if (!((live >> (16 * i + t + 4 * (je & 1) + 8 * (je >> 1))) & 1u))
-                        x[4 * i + je][0] = x[4 * i + je][1] = -INFINITY;
+            for (int j = 0; j < NT; ++j) {
+                if (!((mine >> (8 * j)) & 1u)) x[j][0].x = x[j][1].x = -INFINITY;
+                if (!((mine >> (8 * j + 4)) & 1u)) x[j][0].y = x[j][1].y = -INFINITY;
+            }
         }
     }
 };
@@ -415,7 +465,8 @@ struct QAttend {
 
     QQuery<D, F> q;
     float o[D / 8][4];  // tile j, element e: head gid + 8 (e / 2), dim (2t + e % 2) D / 8 + j
-    float m[2], l[2], zacc[2];  // p = 2^(logit - m); m lies 10..14 below the running maximum
+    float m[2];         // p = 2^(logit - m); m lies 10..14 below the running maximum
+    float2 l[2], zacc[2];       // sums of p and p z' (two shares a lane, a lane's keys)
     float up;                   // power of two above every |scale| seen: O counts in it
 
     __device__ __forceinline__ void init(const __nv_bfloat16* qp, size_t stride, int g,
@@ -425,7 +476,7 @@ struct QAttend {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
             m[hr] = -INFINITY;
-            l[hr] = zacc[hr] = 0.f;
+            l[hr] = zacc[hr] = make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
@@ -451,8 +502,8 @@ struct QAttend {
             const float mn = fmaxf(m[hr], mx[hr] - 10.f);
             const float f = mn == -INFINITY ? 1.f : exp2f(m[hr] - mn);
             m[hr] = mn;
-            l[hr] *= f;
-            zacc[hr] *= f;
+            l[hr] = fmul2(l[hr], both(f));
+            zacc[hr] = fmul2(zacc[hr], both(f));
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
                 o[j][2 * hr] *= f * fo;
@@ -464,23 +515,24 @@ struct QAttend {
     // One stage's keys.  maxima(step, head gid's, head gid + 8's): the step's
     // largest logit per head, log2 domain, the same in a quad.
     template <class Maxima>
-    __device__ __forceinline__ void step(const Ring& ring, int s, uint32_t live, int at,
+    __device__ __forceinline__ void step(const Ring& ring, uint32_t st, uint32_t live, int at,
                                          const Maxima& maxima) {
-        float x[NK / 4][2];
-        q.logits(x, ring, s, live);
+        float2 x[NT][2];
+        q.logits(x, ring, st, live);
         uint32_t ent[NT / 2][4];
         float mx[2], big = 0.f;
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
-            ring.entries(ent[i], s, i, true);
+            ring.entries(ent[i], st, i, true);
 #pragma unroll
-            for (int je = 0; je < 4; ++je) big = fmaxf(big, fabsf(entry_scale(ent[i][je])));
+            for (int je = 0; je < 4; je += 2)
+                big = tc::max3f(big, fabsf(entry_scale(ent[i][je])), fabsf(entry_scale(ent[i][je + 1])));
         }
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-            mx[hr] = x[0][hr];
+            mx[hr] = fmaxf(x[0][hr].x, x[0][hr].y);
 #pragma unroll
-            for (int i = 1; i < NK / 4; ++i) mx[hr] = fmaxf(mx[hr], x[i][hr]);
+            for (int j = 1; j < NT; ++j) mx[hr] = tc::max3f(mx[hr], x[j][hr].x, x[j][hr].y);
             mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
             mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
             mx[hr] *= q.kf[hr];
@@ -488,37 +540,36 @@ struct QAttend {
         maxima(at, mx[0], mx[1]);
         if (__any_sync(0xffffffffu, mx[0] > m[0] + 14.f || mx[1] > m[1] + 14.f || big > up))
             rescale(mx[0], mx[1], big);
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         const float down = up == 0.f ? 0.f : __uint_as_float(0x7f000000u - __float_as_uint(up));
+        const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
 #pragma unroll
         for (int i = 0; i < NT / 2; ++i) {
-            float w[4][2];
+            uint32_t a[4];
 #pragma unroll
-            for (int je = 0; je < 4; ++je) {
-                const float sc = entry_scale(ent[i][je]);
-                float z = entry_zero(ent[i][je]);
-                if constexpr (F == HS_KV_INT4) z = fmaf(8.f, sc, z);
-                const float sd = sc * down;
+            for (int jj = 0; jj < 2; ++jj) {
+                float2 sc, z;
+                entry_pair(ent[i][2 * jj], ent[i][2 * jj + 1], sc, z);
+                sc = fmul2(sc, both(down));
 #pragma unroll
                 for (int hr = 0; hr < 2; ++hr) {
-                    const float p = exp2_approx(fmaf(x[4 * i + je][hr], q.kf[hr], -mu[hr]));
-                    l[hr] += p;
-                    zacc[hr] = fmaf(p, z, zacc[hr]);
-                    w[je][hr] = p * sd;
+                    const float2 y = tc::ffma2(x[2 * i + jj][hr], both(q.kf[hr]), both(nm[hr]));
+                    const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                    l[hr] = tc::fadd2(l[hr], p);
+                    zacc[hr] = tc::ffma2(p, z, zacc[hr]);
+                    const float2 w = fmul2(p, sc);
+                    a[2 * jj + hr] = pack_f16(w.x, w.y);
                 }
             }
-            const uint32_t a[4] = {pack_f16(w[0][0], w[1][0]), pack_f16(w[0][1], w[1][1]),
-                                   pack_f16(w[2][0], w[3][0]), pack_f16(w[2][1], w[3][1])};
             uint32_t v[4][Ring::R::kVW];
 #pragma unroll
-            for (int je = 0; je < 4; ++je) ring.v_words(v[je], s, 16 * i + (threadIdx.x & 3) + 4 * je);
+            for (int je = 0; je < 4; ++je) ring.v_words(v[je], st, i, je);
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 2) {
-                uint32_t b0[2], b1[2];
-                v_pairs<F>(v[0], v[1], j, b0[0], b0[1]);
-                v_pairs<F>(v[2], v[3], j, b1[0], b1[1]);
-                mma_f16(o[j], a, b0[0], b1[0]);
-                mma_f16(o[j + 1], a, b0[1], b1[1]);
+            for (int j = 0; j < D / 8; j += 4) {
+                uint32_t b0[4], b1[4];
+                v_pairs<F>(v[0], v[1], j, b0);
+                v_pairs<F>(v[2], v[3], j, b1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma_f16(o[j + e], a, b0[e], b1[e]);
             }
         }
     }
@@ -550,7 +601,7 @@ struct QAttend {
             cp_async_commit();
             ahead += stride;
             row = mine(ahead);
-            step(ring, s, ring.live(s, src, st * NK), st, maxima);
+            step(ring, ring.stage(s), ring.live(s, src, st * NK), st, maxima);
             s = s + 1 == kStages ? 0 : s + 1;
             fs = fs + 1 == kStages ? 0 : fs + 1;
         }
@@ -559,18 +610,20 @@ struct QAttend {
     }
 
     // Sums over the quad, puts O in its own units and adds the zero points:
-    // o = sum p v^, l = sum p.
+    // o = sum p v^, l[hr].x = sum p.
     __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-            l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
-            l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
-            zacc[hr] += __shfl_xor_sync(0xffffffffu, zacc[hr], 1);
-            zacc[hr] += __shfl_xor_sync(0xffffffffu, zacc[hr], 2);
+            float s = l[hr].x + l[hr].y, z = zacc[hr].x + zacc[hr].y;
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            l[hr].x = s;
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
-                o[j][2 * hr] = fmaf(o[j][2 * hr], up, zacc[hr]);
-                o[j][2 * hr + 1] = fmaf(o[j][2 * hr + 1], up, zacc[hr]);
+                o[j][2 * hr] = fmaf(o[j][2 * hr], up / kCodeUnit<F>, z);
+                o[j][2 * hr + 1] = fmaf(o[j][2 * hr + 1], up / kCodeUnit<F>, z);
             }
         }
     }
@@ -585,7 +638,7 @@ struct QAttend {
             if (h >= g) continue;
             if (t == 0) {
                 part[2 * h] = m[hr];
-                part[2 * h + 1] = l[hr];
+                part[2 * h + 1] = l[hr].x;
             }
             float* row = part + 32 + h * D + t * (D / 4);
 #pragma unroll

@@ -28,7 +28,7 @@ __device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o,
     for (int hr = 0; hr < 2; ++hr) {
         const int h = gid + 8 * hr;
         if (h >= g) continue;
-        const float inv = st.l[hr] == 0.f ? 0.f : 1.f / st.l[hr];
+        const float inv = st.l[hr].x == 0.f ? 0.f : 1.f / st.l[hr].x;
         const size_t row = head0 + h * stride;
         __nv_bfloat16* dst = o + row * D + t * (D / 4);
 #pragma unroll
@@ -42,7 +42,7 @@ __device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o,
                                      st.o[j + 2 * i + 1][2 * hr + e] * inv);
                 *reinterpret_cast<uint4*>(dst + e * (D / 8) + j) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-        if (t == 0) lse[row] = st.l[hr] == 0.f ? -INFINITY : (st.m[hr] + log2f(st.l[hr])) * kLn2;
+        if (t == 0) lse[row] = st.l[hr].x == 0.f ? -INFINITY : (st.m[hr] + log2f(st.l[hr].x)) * kLn2;
     }
 }
 
