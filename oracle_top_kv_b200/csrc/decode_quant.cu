@@ -31,12 +31,17 @@ namespace dq {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 640;  // partial slots reserved: at most kMaxCtas + units
-template <int D, int F> using Attend = QAttend<D, F, kStages>;
+template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages>;
+// Four-warp CTAs of the full kernel to an SM that the registers are divided for.
+template <int NH> constexpr int kPerSm = NH == 1 ? 4 : 2;
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBoundCap = 16384;  // tile bounds a selecting CTA holds on chip
 template <int D, int F> using SelRing = QRing<D, F, false, 3>;
+// Rounds of rescoring between looks at the number of candidates, where the buffer for
+// that many fits (budgets k - w up to about 3000); else 1.
+constexpr int kCheck = 4;
 
 constexpr int kBitsPad = 512;     // the tiles are dealt out in chunks of 32 to up to 8 CTAs
 
@@ -96,24 +101,39 @@ __device__ __forceinline__ int share_of(long long x, int G, long long total) {
     return (int)(((x + 1) * G - 1) / total);
 }
 
-// Stores each step's maxima: lanes t = 0 of a warp hold a head pair each.
+// Reduces each step's maxima over the keys and stores them: each halving of the
+// lanes of equal t drops half of the lane's heads.
 struct TileMaxima {
     float* at;  // this unit's [tiles][16]
-    __device__ __forceinline__ void operator()(int step, float m0, float m1) const {
+    template <int NH>
+    __device__ __forceinline__ void operator()(int step, const float2 (&m)[NH]) const {
         const int lane = threadIdx.x & 31;
-        if ((lane & 3) == 0) {
-            float* r = at + (size_t)step * 16 + (lane >> 2);
-            r[0] = m0;
-            r[8] = m1;
+        auto halve = [&](float a, float b, int bit) {  // a where the bit is clear
+            const float got = __shfl_xor_sync(0xffffffffu, lane & bit ? a : b, bit);
+            return fmaxf(lane & bit ? b : a, got);
+        };
+        float v;
+        int h = 2 * (lane & 3);
+        if constexpr (NH == 2) {
+            const float x = halve(m[0].x, m[1].x, 16), y = halve(m[0].y, m[1].y, 16);
+            v = halve(x, y, 8);
+            h += (lane & 16 ? 8 : 0) + (lane & 8 ? 1 : 0);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        } else {
+            v = halve(m[0].x, m[0].y, 16);
+            h += lane & 16 ? 1 : 0;
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         }
+        if (!(lane & (NH == 2 ? 4 : 12))) at[(size_t)step * 16 + h] = v;
     }
 };
 
-template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+template <int D, int F, int NH>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     decode_quant_full_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                              const int32_t* __restrict__ seq_len, Ws ws) {
-    using A = Attend<D, F>;
+    using A = Attend<D, F, NH>;
     constexpr int NK = A::NK;
     extern __shared__ __align__(16) unsigned char smem_raw[];  // rings, reused for partials
     constexpr int kStride = A::Ring::kBytes / 4;
@@ -327,14 +347,14 @@ struct QKeys {
 };
 
 // Rescores a source's keys, warp w of the CTA steps w, w + kSelWarps, ...: put(key,
-// score, log2 domain) for each; after_round() once per round, by all threads.
-template <int D, int F, class Src, class Put, class After>
-__device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&lse2)[2],
+// score, log2 domain) for each; after_rounds() by all threads, once per `check` rounds.
+template <int D, int F, int NH, class Src, class Put, class After>
+__device__ __forceinline__ void score_keys(const QQuery<D, F, NH>& q, const float2 (&lse2)[NH],
                                            uint32_t ring_base, const QuantCache& c, const Src& src,
-                                           int n_steps, Put put, After after_round) {
+                                           int n_steps, int check, Put put, After after_rounds) {
     using Ring = SelRing<D, F>;
     constexpr int NK = Ring::NK;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
     const Ring ring{ring_base + warp * Ring::kBytes};
     auto mine = [&](int st) { return st < n_steps ? src.row(st * NK + (lane & (NK - 1))) : -1; };
     int row = mine(warp), ahead = warp;
@@ -345,7 +365,7 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&
         ahead += kSelWarps;
         row = mine(ahead);
     }
-    int s = 0;
+    int s = 0, rounds = 0;
     for (int r0 = 0; r0 < n_steps; r0 += kSelWarps) {
         const int st = r0 + warp;
         cp_async_wait<1>();
@@ -356,33 +376,29 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F>& q, const float (&
         row = mine(ahead);
         if (st < n_steps) {
             const uint32_t live = ring.live(s, src, st * NK);
-            float2 x[NK / 8][2];
+            float2 x[NK / 16][2][NH];
             q.logits(x, ring, ring.stage(s), live);
 #pragma unroll
-            for (int i = 0; i < NK / 16; ++i) {
-                // v[je]: key t + 4 je of the group, this lane's two heads; then the
-                // maximum over gid, each halving of the lanes dropping half the keys
-                float v[4];
+            for (int i = 0; i < NK / 16; ++i)
 #pragma unroll
-                for (int je = 0; je < 4; ++je) {
-                    const float2(&y)[2] = x[2 * i + (je >> 1)];
-                    const float y0 = je & 1 ? y[0].y : y[0].x, y1 = je & 1 ? y[1].y : y[1].x;
-                    v[je] = fmaxf(fmaxf(-INFINITY, __fsub_rn(__fmul_rn(y0, q.kf[0]), lse2[0])),
-                                  __fsub_rn(__fmul_rn(y1, q.kf[1]), lse2[1]));
+                for (int k = 0; k < 2; ++k) {
+                    // the best of the quad's heads: NaN loses
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+                        v = tc::max3f(v, __fsub_rn(__fmul_rn(x[i][k][n].x, q.kf[n].x), lse2[n].x),
+                                      __fsub_rn(__fmul_rn(x[i][k][n].y, q.kf[n].y), lse2[n].y));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    const int slot = 16 * i + 8 * k + (gid >> 1) + 4 * (gid & 1);
+                    if (t == 0 && ((live >> slot) & 1u)) put(src.key(st * NK + slot), v);
                 }
-                const bool up = lane & 16, up2 = lane & 8;
-                const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
-                const float b = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
-                const float w0 = fmaxf(up ? v[2] : v[0], a), w1 = fmaxf(up ? v[3] : v[1], b);
-                const float d = __shfl_xor_sync(0xffffffffu, up2 ? w0 : w1, 8);
-                float e = fmaxf(up2 ? w1 : w0, d);
-                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4));
-                const int slot = 16 * i + t + 4 * (2 * (up ? 1 : 0) + (up2 ? 1 : 0));
-                if (!(lane & 4) && ((live >> slot) & 1u)) put(src.key(st * NK + slot), e);
-            }
         }
         s = s == 2 ? 0 : s + 1;
-        after_round();
+        if (++rounds == check) {
+            rounds = 0;
+            after_rounds();
+        }
     }
     cp_async_wait<0>();
     __syncwarp();
@@ -402,6 +418,51 @@ __device__ void keep_largest(uint64_t* buf, int n, int K, uint64_t* tmp, CtaSele
     *kth_out = kth;
 }
 
+// Ascending sort of a[0 .. n), n a power of two up to 4096, by kSelThreads threads: bitonic;
+// exchanges within a warp's 64 values stay in registers (of 55 steps for 1024
+// values 10 go through shared memory).
+__device__ void sort_ascending(uint64_t* a, int n) {
+    const int lane = threadIdx.x & 31;
+    for (int base = threadIdx.x - lane; base * 2 < n; base += kSelThreads) {
+        // a warp's 64 values, two a lane (i and i + 32)
+        uint64_t* w = a + base * 2;
+        uint64_t x = base * 2 + lane < n ? w[lane] : ~0ull;
+        uint64_t y = base * 2 + lane + 32 < n ? w[lane + 32] : ~0ull;
+        warp_sort64(x, y);
+        const bool down = (base * 2) & 64;  // alternate runs of 64 descend
+        if (base * 2 + lane < n) w[down ? 63 - lane : lane] = x;
+        if (base * 2 + lane + 32 < n) w[down ? 31 - lane : lane + 32] = y;
+    }
+    __syncthreads();
+    for (int k = 128; k <= n; k <<= 1) {
+        int j = k >> 1;
+        for (; j >= 64; j >>= 1) {
+            for (int i = threadIdx.x; i < n / 2; i += kSelThreads) {
+                const int p = 2 * i - (i & (j - 1)), q = p + j;
+                const uint64_t x = a[p], y = a[q];
+                if ((x > y) == ((p & k) == 0)) { a[p] = y; a[q] = x; }
+            }
+            __syncthreads();
+        }
+        for (int base = threadIdx.x - lane; base * 2 < n; base += kSelThreads) {
+            uint64_t* w = a + base * 2;
+            uint64_t x = w[lane], y = w[lane + 32];
+            const bool up = ((base * 2) & k) == 0;
+            if ((x > y) == up) { const uint64_t z = x; x = y; y = z; }
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1) {
+                const uint64_t px = shfl_xor_u64(x, s), py = shfl_xor_u64(y, s);
+                const bool low = ((lane & s) == 0) == up;  // keeps the smaller
+                x = low == (x < px) ? x : px;
+                y = low == (y < py) ? y : py;
+            }
+            w[lane] = x;
+            w[lane + 32] = y;
+        }
+        __syncthreads();
+    }
+}
+
 // Dynamic shared memory of the selection, for Kc = k - w.
 template <int D, int F>
 struct SelSmem {
@@ -409,22 +470,24 @@ struct SelSmem {
         (size_t)kSelWarps * SelRing<D, F>::kBytes > sizeof(uint32_t) * kBoundCap
             ? (size_t)kSelWarps * SelRing<D, F>::kBytes
             : sizeof(uint32_t) * kBoundCap;
-    static constexpr int kRound = kSelWarps * SelRing<D, F>::NK;  // keys offered per round
-    __host__ __device__ static int cap(int Kc) { return 2 * Kc + kRound; }
+    static constexpr int kRound = kSelWarps * SelRing<D, F>::NK;  // keys of a round
+    __host__ __device__ static int cap(int Kc, int check) { return 2 * Kc + check * kRound; }
     __host__ __device__ static int sort_n(int Kc) { return next_pow2(Kc > 0 ? Kc : 1); }
-    __host__ __device__ static size_t bytes(int Kc) {
-        return kFront + sizeof(uint64_t) * (cap(Kc) + sort_n(Kc)) + sizeof(int) * (Kc + 2);
+    __host__ __device__ static size_t bytes(int Kc, int check) {
+        return kFront + sizeof(uint64_t) * (cap(Kc, check) + sort_n(Kc)) + sizeof(int) * (Kc + 2);
     }
+    static constexpr size_t kMost = 232448 - 4096;  // a CTA's shared memory, less the static part
+    static int check(int Kc) { return bytes(Kc, kCheck) <= kMost ? kCheck : 1; }
 };
 
-template <int D, int F>
+template <int D, int F, int NH>
 __global__ void __launch_bounds__(kSelThreads, 1)
     decode_quant_select_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
-                               const int32_t* __restrict__ seq_len, Ws ws, int grid1, int C,
+                               const int32_t* __restrict__ seq_len, Ws ws, int grid1, int C, int check,
                                __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
                                int32_t* __restrict__ idx, int32_t* __restrict__ cnt,
                                float* __restrict__ sel) {
-    using A = Attend<D, F>;
+    using A = Attend<D, F, NH>;
     using S = SelSmem<D, F>;
     constexpr int NK = A::NK;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -432,7 +495,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     __shared__ float s_m[16], s_lse2[16];
     __shared__ int s_n, s_list, s_cut;
     __shared__ unsigned long long s_thr;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, g = p.group;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3, g = p.group;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int unit = blockIdx.x / C, u = unit % p.hkv, b = unit / p.hkv;
     const int L = __ldg(seq_len + b);
@@ -452,6 +515,8 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         return;
     }
     // ---- merge of the unit's partials
+    if (tid < 16) s_lse2[tid] = INFINITY;  // heads past the group never score
+    __syncthreads();
     {
         const long long before = sum_steps<NK>(seq_len, 0, b, p.t_kv);
         const long long total = (before + sum_steps<NK>(seq_len, b, p.batch, p.t_kv)) * p.hkv;
@@ -525,14 +590,17 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     const PageMap pm = page_map(p, b, u);
     const bool paged = p.bt != nullptr;
     uint64_t* buf = reinterpret_cast<uint64_t*>(smem_raw + S::kFront);  // [cap(Kc)]
-    uint64_t* tmp = buf + S::cap(Kc);                                    // [sort_n(Kc)]
+    uint64_t* tmp = buf + S::cap(Kc, check);                                    // [sort_n(Kc)]
     int* list = reinterpret_cast<int*>(tmp + S::sort_n(Kc));             // [Kc + 2]
-    QQuery<D, F> qq;
-    float nl[2];
+    QQuery<D, F, NH> qq;
+    float2 nl[NH];
     if (ranked || srow) {
         qq.init(q + head0 * D, D, g, p.scale_log2);
-        nl[0] = gid < g ? s_lse2[gid] : INFINITY;
-        nl[1] = gid + 8 < g ? s_lse2[gid + 8] : INFINITY;
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int h = 8 * n + 2 * t;
+            nl[n] = make_float2(s_lse2[h], s_lse2[h + 1]);
+        }
     }
     if (tid == 0) { s_n = 0; s_list = 0; s_thr = 0ull; }
     __syncthreads();
@@ -552,21 +620,31 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                                                : ws.bits + (size_t)unit * (ws.tiles + kBitsPad) +
                                                      (size_t)rank * ((chunks + C - 1) / C) * 32;
             // a CTA may hold up to 31 places past its tiles: they rank last
-            for (int i = tid; i < mine; i += blockDim.x) {
-                const int x = tile(i);
-                float v = -INFINITY;
-                if (x < full) {
+            constexpr int U = 2, Q4 = 2 * NH;  // tiles in flight per thread, float4 of a tile
+            for (int i0 = tid; i0 < mine; i0 += U * kSelThreads) {
+                float4 a[U][Q4];
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        if (4 * q4 >= g) break;
-                        const float4 a = __ldg(tm + (size_t)x * 4 + q4);
-                        const float av[4] = {a.x, a.y, a.z, a.w};
+                for (int k = 0; k < U; ++k) {
+                    const int i = i0 + k * kSelThreads, x = tile(i);
+#pragma unroll
+                    for (int q4 = 0; q4 < Q4; ++q4)
+                        a[k][q4] = i < mine && x < full ? __ldg(tm + (size_t)x * 4 + q4)
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int i = i0 + k * kSelThreads;
+                    if (i >= mine) break;
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int q4 = 0; q4 < Q4; ++q4) {
+                        const float av[4] = {a[k][q4].x, a[k][q4].y, a[k][q4].z, a[k][q4].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (4 * q4 + e < g) v = fmaxf(v, __fsub_rn(av[e], s_lse2[4 * q4 + e]));
+                            v = fmaxf(v, __fsub_rn(av[e], s_lse2[4 * q4 + e]));
                     }
+                    bits[i] = tile(i) < full ? float_order(v) : 0u;
                 }
-                bits[i] = x < full ? float_order(v) : 0u;
             }
             __syncthreads();
             auto key = [&](int i) -> uint64_t {
@@ -588,9 +666,9 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         if (tid == 0 && rank == 0 && lo % NK != 0) list[s_list++] = full;
         __syncthreads();
         const QTiles<NK> src{list, s_list, lo, paged, pm};
-        const int cap = S::cap(Kc);
-        score_keys<D, F>(
-            qq, nl, smem_u32(smem_raw), uc, src, s_list,
+        const int cap = S::cap(Kc, check);
+        score_keys<D, F, NH>(
+            qq, nl, smem_u32(smem_raw), uc, src, s_list, check,
             [&](int key, float v) {
                 const uint64_t c = sel_key(v, (uint32_t)key);
                 if (c >= s_thr) buf[atomicAdd(&s_n, 1)] = c;
@@ -599,7 +677,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                 __syncthreads();
                 const int have = s_n;
                 __syncthreads();  // read by all before the next offers
-                if (have > cap - S::kRound) {
+                if (have > cap - check * S::kRound) {
                     uint64_t kth;
                     keep_largest(buf, have, Kc, tmp, cs, &s_cut, &kth);
                     if (tid == 0) { s_thr = kth; s_n = Kc; }
@@ -635,7 +713,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         for (int x = tid; x < sort_n; x += blockDim.x)
             tmp[x] = x < n_best ? ((uint64_t)sel_key_id(buf[x]) << 32) | (buf[x] >> 32) : ~0ull;
         __syncthreads();
-        cta_bitonic_sort(tmp, sort_n);
+        sort_ascending(tmp, sort_n);
         for (int x = tid; x < n_best; x += blockDim.x) {
             irow[x] = (int32_t)(tmp[x] >> 32);
             if (srow) srow[x] = exp2f(order_float((uint32_t)tmp[x]));
@@ -650,15 +728,15 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     if (tid == 0) cnt[unit] = n_out;
     if (srow) {
         __syncthreads();
-        score_keys<D, F>(
-            qq, nl, smem_u32(smem_raw), uc, QKeys{lo, L, paged, pm}, (L - lo + NK - 1) / NK,
+        score_keys<D, F, NH>(
+            qq, nl, smem_u32(smem_raw), uc, QKeys{lo, L, paged, pm}, (L - lo + NK - 1) / NK, 1,
             [&](int key, float v) { srow[n_best + key - lo] = exp2f(v); }, [] {});
     }
 }
 
 // CTAs of the full kernel that fill the current device once, and its SMs
 // (cached per device).
-template <int D, int F>
+template <int D, int F, int NH>
 static cudaError_t full_grid(size_t smem, int* ctas, int* sms) {
     static std::atomic<int> known[64];
     int dev = 0;
@@ -670,7 +748,7 @@ static cudaError_t full_grid(size_t smem, int* ctas, int* sms) {
     if (n == 0) {
         int per = 0;
         if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                 &per, decode_quant_full_kernel<D, F>, kWarps * 32, smem)) != cudaSuccess)
+                 &per, decode_quant_full_kernel<D, F, NH>, kWarps * 32, smem)) != cudaSuccess)
             return e;
         n = min(kMaxCtas, max(1, per) * *sms);
         if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
@@ -679,29 +757,30 @@ static cudaError_t full_grid(size_t smem, int* ctas, int* sms) {
     return cudaSuccess;
 }
 
-template <int D, int F>
+template <int D, int F, int NH>
 static cudaError_t launch_t(const KParams& p, const QuantCache& c, const void* q_,
                             const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,
                             float* lse, float* sel, void* ws_, cudaStream_t st) {
-    using A = Attend<D, F>;
+    using A = Attend<D, F, NH>;
     const __nv_bfloat16* q = (const __nv_bfloat16*)q_;
     const Ws w = ws_layout(p, ws_);
     const int units = p.batch * p.hkv;
     cudaError_t e;
-    auto full = decode_quant_full_kernel<D, F>;
+    auto full = decode_quant_full_kernel<D, F, NH>;
     const size_t smem = (size_t)kWarps * A::Ring::kBytes;
     if ((e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
         cudaSuccess)
         return e;
     int G = 0, sms = 148;
-    if ((e = full_grid<D, F>(smem, &G, &sms)) != cudaSuccess) return e;
+    if ((e = full_grid<D, F, NH>(smem, &G, &sms)) != cudaSuccess) return e;
     // no CTA below a step per warp, as far as the capacity tells
     const int steps = (p.t_kv + A::NK - 1) / A::NK;
     G = (int)max(1ll, min((long long)G, ((long long)units * steps + kWarps - 1) / kWarps));
     full<<<G, kWarps * 32, smem, st>>>(p, c, q, seq_len, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    auto select = decode_quant_select_kernel<D, F>;
-    const size_t s1 = SelSmem<D, F>::bytes(p.k - p.window);
+    auto select = decode_quant_select_kernel<D, F, NH>;
+    const int check = SelSmem<D, F>::check(p.k - p.window);
+    const size_t s1 = SelSmem<D, F>::bytes(p.k - p.window, check);
     if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) !=
         cudaSuccess)
         return e;
@@ -721,9 +800,25 @@ static cudaError_t launch_t(const KParams& p, const QuantCache& c, const void* q
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, select, p, c, q, seq_len, w, G, C, (__nv_bfloat16*)o, lse, idx,
+    return cudaLaunchKernelEx(&cfg, select, p, c, q, seq_len, w, G, C, check, (__nv_bfloat16*)o, lse, idx,
                               cnt, sel);
 }
+
+struct Launch {
+    const KParams& p;
+    const QuantCache& c;
+    const void* q;
+    const int32_t* seq_len;
+    int32_t *idx, *cnt;
+    void* o;
+    float *lse, *sel;
+    void* ws;
+    cudaStream_t st;
+    template <int D, int F, int NH>
+    cudaError_t operator()() const {
+        return launch_t<D, F, NH>(p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st);
+    }
+};
 
 }  // namespace dq
 
@@ -732,13 +827,7 @@ size_t decode_quant_workspace(const KParams& p) { return dq::ws_layout(p, nullpt
 cudaError_t launch_decode_quant(const KParams& p, int format, const QuantCache& c, const void* q,
                                 const int32_t* seq_len, int32_t* idx, int32_t* cnt, void* o,
                                 float* lse, float* sel, void* ws, cudaStream_t st) {
-    if (format == HS_KV_INT4)
-        return p.head_dim == 64
-                   ? dq::launch_t<64, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st)
-                   : dq::launch_t<128, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st);
-    return p.head_dim == 64
-               ? dq::launch_t<64, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st)
-               : dq::launch_t<128, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st);
+    return sq::dispatch(p, format, dq::Launch{p, c, q, seq_len, idx, cnt, o, lse, sel, ws, st});
 }
 
 }  // namespace hs

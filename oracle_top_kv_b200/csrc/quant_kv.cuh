@@ -27,14 +27,16 @@
 // 12.8, with 8 of them 17), so 16 keys of 128 dims take 256 issue cycles for their
 // 32 MMAs beside some 250 for unpacking, the softmax and the reads.
 //
-// One warp, 16 heads as the rows of mma.m16n8k16, 16 keys at a time.  Lane
-// (gid, t) of the warp (gid = lane / 4, t = lane % 4) needs of a key's K row the
+// One warp takes 16 keys at a time: they are the rows of S^T = K Q^T, 8 heads at a
+// time its columns, and O^T = V^T P^T has 16 dimensions at a time as rows (P^T's
+// fragments from movmatrix), so that groups of up to 8 heads need half the MMAs of 16.
+// Lane (gid, t) of the warp (gid = lane / 4, t = lane % 4) needs of a key's K row the
 // t-th quarter and of a V row the gid-th eighth (Q's fragments take the same
 // order of dimensions), so rows are read from shared memory as they lie in the
 // cache.  cp.async fills a ring of stages per warp; it also places the rows:
-// within 16 keys, key t + 4 e + 8 j is column 2 t + e of 8-column tile j, K rows lie in
-// column order, V rows keep their order with 16-byte chunks swizzled, a lane's
-// four entries are adjacent: every shared read is free of bank conflicts.
+// within 16 keys, key t + 4 e + 8 j is row 2 t + e of the j-th 8 rows; K rows lie in
+// that order, V rows keep their own with 16-byte chunks swizzled, and the four entries
+// of equal t are adjacent: every shared read of rows is free of bank conflicts.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -191,7 +193,7 @@ struct QRing {
         constexpr int PER = 16 / (RB / 8) > 0 ? 16 / (RB / 8) : 1;  // eighths per chunk
         k_at = (uint32_t)(gid * RB + (RB == 128 ? ((2 * t) ^ (gid & 1)) << 4 : t * (RB / 4)));
         v_at = (uint32_t)(kHalf + v_slot(t, gid / PER) + (gid % PER) * (RB / 8));
-        e_at = (uint32_t)(kKeyBytes + 16 * t);
+        e_at = (uint32_t)(kKeyBytes + 16 * (gid >> 1) + 4 * (gid & 1));
         k_to = k_slot(row, ch);
         v_to = kHalf + v_slot(row, ch);
         e_to = (uint32_t)(kKeyBytes + 4 * ((lane & ~15) + 4 * (lane & 3) + ((lane >> 2) & 3)));
@@ -310,7 +312,7 @@ struct QRing {
                          : "r"(a)
                          : "memory");
     }
-    // Lane's quarter of the K row in column gid of tile j.
+    // Lane's quarter of the K row in row gid of the j-th 8 rows.
     __device__ __forceinline__ void k_words(uint32_t (&w)[R::kKW], uint32_t st, int j) const {
         const uint32_t a = st + k_at + (uint32_t)(8 * j * RB);
         if constexpr (R::kKW == 8) {
@@ -330,9 +332,11 @@ struct QRing {
     __device__ __forceinline__ void v_words(uint32_t (&w)[R::kVW], uint32_t st, int i, int je) const {
         lds<R::kVW>(w, st + v_at + (uint32_t)((16 * i + 4 * je) * RB));
     }
-    // Entries of keys t, t + 4, t + 8, t + 12 of 16-key group i.
-    __device__ __forceinline__ void entries(uint32_t (&e)[4], uint32_t st, int i, bool v) const {
-        lds<4>(e, st + e_at + (v ? kHalf : 0) + 64u * i);
+    // Entry of row gid + 8 k of 16-key group i.
+    __device__ __forceinline__ uint32_t entry(uint32_t st, int i, int k, bool v) const {
+        uint32_t e[1];
+        lds<1>(e, st + e_at + (v ? kHalf : 0) + 64u * i + 8u * k);
+        return e[0];
     }
 };
 
@@ -347,33 +351,37 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Scales and zero points of two entries.
-__device__ __forceinline__ void entry_pair(uint32_t e0, uint32_t e1, float2& sc, float2& z) {
-    sc = make_float2(entry_scale(e0), entry_scale(e1));
-    z = make_float2(entry_zero(e0), entry_zero(e1));
+// 8 x 8 transpose of b16 pairs over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 // ---------------------------------------------------------------- attention
-// A warp's query: 16 heads of a unit.
-template <int D, int F>
+// A warp's query: NH * 8 heads of a unit.  kShared: its fragments lie in shared memory
+// (kBytes of it), for kernels that want the registers for a further CTA on the SM.
+template <int D, int F, int NH, bool kShared = false>
 struct QQuery {
-    uint32_t qf[D / 16][4];
-    float qsum[2];  // sum of the scaled q in units of the operands, heads gid and gid + 8
-    float kf[2];    // logit of the scaled q -> log2 domain
+    static constexpr int kBytes = kShared ? D / 16 * NH * 256 : 0;
+    uint32_t qb[kShared ? 1 : NH][kShared ? 1 : D / 16][2];  // B fragments of 8 heads each
+    uint32_t at = 0;                                         // this lane's, if shared
+    float2 qsum[NH];  // sums of the scaled q in units of the operands, heads 8 n + 2 t, + 1
+    float2 kf[NH];    // logits of the scaled q -> log2 domain
 
-    // q: the unit's query rows, `stride` elements apart; rows g..15 are zero.
+    // q: the unit's query rows, `stride` elements apart; rows from g on are zero.
     __device__ __forceinline__ void init(const __nv_bfloat16* q, size_t stride, int g,
-                                         float scale_log2) {
+                                         float scale_log2, uint32_t shared_at = 0) {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
+        at = shared_at + lane * 8;  // a lane reads what it wrote
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            const bool ok = gid + 8 * hr < g;
+        for (int n = 0; n < NH; ++n) {
+            const int h = 8 * n + gid;
             float x[D / 4], amax = 0.f;
-            const uint4* src =
-                reinterpret_cast<const uint4*>(q + (size_t)(gid + 8 * hr) * stride + t * (D / 4));
+            const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)h * stride + t * (D / 4));
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const uint4 v = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = h < g ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -388,8 +396,8 @@ struct QQuery {
             // 2^(14 - exponent); the exponent is held above -100, where q still fits
             const int ex = max((int)(__float_as_uint(amax) >> 23), 27) - 127;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            kf[hr] = fmaxf(scale_log2 / kCodeUnit<F> *
-                               __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
+            const float k = fmaxf(scale_log2 / kCodeUnit<F> *
+                                      __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) {
@@ -398,96 +406,132 @@ struct QQuery {
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            qsum[hr] = sum * kCodeUnit<F>;
+            sum *= kCodeUnit<F>;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qf[ks][2 * e + hr] = pack_f16(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = pack_f16(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
+                    if constexpr (kShared)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + (ks * NH + n) * 256 + 4 * e),
+                                     "r"(w) : "memory");
+                    else qb[n][ks][e] = w;
+                }
+            qsum[n] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
+                                  __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+            kf[n] = make_float2(__shfl_sync(0xffffffffu, k, 8 * t),
+                                __shfl_sync(0xffffffffu, k, 8 * t + 4));
         }
     }
 
-    // Logits, before kf, of the stage's keys: x[j][hr] of keys t + 8 j (.x) and t + 4
-    // + 8 j (.y) past each 16 (j even: the first 8 of them) and head gid + 8 hr; -inf
-    // where `live` is clear.
+    // Logits, before kf, of the stage's keys: x[i][k][n] of row gid + 8 k of 16-key
+    // group i and heads 8 n + 2 t, + 1; -inf where `live` is clear.
     template <class Ring>
-    __device__ __forceinline__ void logits(float2 (&x)[Ring::NK / 8][2], const Ring& ring,
+    __device__ __forceinline__ void logits(float2 (&x)[Ring::NK / 16][2][NH], const Ring& ring,
                                            uint32_t st, uint32_t live) const {
-        constexpr int NT = Ring::NK / 8;
-        float acc[NT][4];
+        constexpr int NG = Ring::NK / 16;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int i = 0; i < NG; ++i) {
+            float acc[NH][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-            uint32_t w[Ring::R::kKW];
-            ring.k_words(w, st, j);
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+            uint32_t w0[Ring::R::kKW], w1[Ring::R::kKW];
+            ring.k_words(w0, st, 2 * i);
+            ring.k_words(w1, st, 2 * i + 1);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t b0, b1;
-                k_frag<F>(w, ks, b0, b1);
-                mma_f16(acc[j], qf[ks], b0, b1);
+                uint32_t a[4];
+                k_frag<F>(w0, ks, a[0], a[2]);
+                k_frag<F>(w1, ks, a[1], a[3]);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    uint32_t b[2];
+                    if constexpr (kShared) {
+                        Ring::template lds<2>(b, at + (ks * NH + n) * 256);
+                    } else {
+                        b[0] = qb[n][ks][0];
+                        b[1] = qb[n][ks][1];
+                    }
+                    mma_f16(acc[n], a, b[0], b[1]);
+                }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) {
-            uint32_t ent[4];
-            ring.entries(ent, st, i, false);
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t ent = ring.entry(st, i, k, false);
+                const float2 sc = both(entry_scale(ent)), z = both(entry_zero(ent));
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                float2 sc, z;
-                entry_pair(ent[2 * jj], ent[2 * jj + 1], sc, z);
-                const float* a = acc[2 * i + jj];
-#pragma unroll
-                for (int hr = 0; hr < 2; ++hr)
-                    x[2 * i + jj][hr] = tc::ffma2(make_float2(a[2 * hr], a[2 * hr + 1]), sc,
-                                                  fmul2(both(qsum[hr]), z));
+                for (int n = 0; n < NH; ++n)
+                    x[i][k][n] = tc::ffma2(make_float2(acc[n][2 * k], acc[n][2 * k + 1]), sc,
+                                           fmul2(qsum[n], z));
             }
         }
         if (live != (Ring::NK == 32 ? 0xffffffffu : 0xffffu)) {
-            const uint32_t mine = live >> (threadIdx.x & 3);
+            const int gid = (threadIdx.x & 31) >> 2;
+            const uint32_t mine = live >> ((gid >> 1) + 4 * (gid & 1));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (!((mine >> (8 * j)) & 1u)) x[j][0].x = x[j][1].x = -INFINITY;
-                if (!((mine >> (8 * j + 4)) & 1u)) x[j][0].y = x[j][1].y = -INFINITY;
-            }
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (!((mine >> (16 * i + 8 * k)) & 1u)) {
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) x[i][k][n] = both(-INFINITY);
+                    }
         }
     }
 };
 
 struct NoMaxima {
-    __device__ __forceinline__ void operator()(int, float, float) const {}
+    template <int NH>
+    __device__ __forceinline__ void operator()(int, const float2 (&)[NH]) const {}
 };
 
-template <int D, int F, int kStages>
+template <int D, int F, int NH, int kStages, bool kSharedQ = false>
 struct QAttend {
     using Ring = QRing<D, F, true, kStages>;
-    static constexpr int NK = Ring::NK, NT = NK / 8;
+    static constexpr int NK = Ring::NK, NG = NK / 16;
 
-    QQuery<D, F> q;
-    float o[D / 8][4];  // tile j, element e: head gid + 8 (e / 2), dim (2t + e % 2) D / 8 + j
-    float m[2];         // p = 2^(logit - m); m lies 10..14 below the running maximum
-    float2 l[2], zacc[2];       // sums of p and p z' (two shares a lane, a lane's keys)
-    float up;                   // power of two above every |scale| seen: O counts in it
+    QQuery<D, F, NH, kSharedQ> q;
+    // tile m: rows dims gid D / 8 + 2 m (elements 0, 1) and + 1 (2, 3), columns heads 8 n
+    // + 2 t, + 1
+    float o[D / 16][NH][4];
+    float2 m[NH];             // p = 2^(logit - m); m lies 10..14 below the running maximum
+    float2 l[NH], zacc[NH];   // sums of p and p z over the lane's keys
+    float up;                 // power of two above every |scale| seen: O counts in it
 
     __device__ __forceinline__ void init(const __nv_bfloat16* qp, size_t stride, int g,
-                                         float scale_log2) {
-        q.init(qp, stride, g, scale_log2);
+                                         float scale_log2, uint32_t shared_q = 0) {
+        q.init(qp, stride, g, scale_log2, shared_q);
         up = 0.f;
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            m[hr] = -INFINITY;
-            l[hr] = zacc[hr] = make_float2(0.f, 0.f);
+        for (int n = 0; n < NH; ++n) {
+            m[n] = both(-INFINITY);
+            l[n] = zacc[n] = both(0.f);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][n][e] = 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     }
 
-    // Moves the references to the step's maxima (log2 domain) and largest |scale|.
-    __device__ __forceinline__ void rescale(float mx0, float mx1, float sc) {
+    __device__ static __forceinline__ float moved(float old, float mx, float& f) {
+        const float mn = fmaxf(old, mx - 10.f);
+        f = mn == -INFINITY ? 1.f : exp2f(old - mn);
+        return mn;
+    }
+    // Moves the references to the step's maxima (log2 domain) and largest |scale|;
+    // mx, sc: the lane's keys'.
+    __device__ __forceinline__ void rescale(float2 (&mx)[NH], float sc) {
 #pragma unroll
-        for (int w = 1; w < 32; w <<= 1) sc = fmaxf(sc, __shfl_xor_sync(0xffffffffu, sc, w));
+        for (int w = 4; w < 32; w <<= 1) {
+            sc = fmaxf(sc, __shfl_xor_sync(0xffffffffu, sc, w));
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                mx[n].x = fmaxf(mx[n].x, __shfl_xor_sync(0xffffffffu, mx[n].x, w));
+                mx[n].y = fmaxf(mx[n].y, __shfl_xor_sync(0xffffffffu, mx[n].y, w));
+            }
+        }
         float fo = 1.f;
         if (sc > up) {
             // 2^(exponent + 1), between 2^-125 and 2^126
@@ -496,68 +540,73 @@ struct QAttend {
             fo = up / nu;
             up = nu;
         }
-        const float mx[2] = {mx0, mx1};
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            const float mn = fmaxf(m[hr], mx[hr] - 10.f);
-            const float f = mn == -INFINITY ? 1.f : exp2f(m[hr] - mn);
-            m[hr] = mn;
-            l[hr] = fmul2(l[hr], both(f));
-            zacc[hr] = fmul2(zacc[hr], both(f));
+        for (int n = 0; n < NH; ++n) {
+            float2 f;
+            m[n].x = moved(m[n].x, mx[n].x, f.x);
+            m[n].y = moved(m[n].y, mx[n].y, f.y);
+            l[n] = fmul2(l[n], f);
+            zacc[n] = fmul2(zacc[n], f);
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                o[j][2 * hr] *= f * fo;
-                o[j][2 * hr + 1] *= f * fo;
-            }
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][n][e] *= (e & 1 ? f.y : f.x) * fo;
         }
     }
 
-    // One stage's keys.  maxima(step, head gid's, head gid + 8's): the step's
-    // largest logit per head, log2 domain, the same in a quad.
+    // One stage's keys.  maxima(step, .): the largest logits (log2 domain) of the lane's
+    // keys, heads 8 n + 2 t, + 1.
     template <class Maxima>
     __device__ __forceinline__ void step(const Ring& ring, uint32_t st, uint32_t live, int at,
                                          const Maxima& maxima) {
-        float2 x[NT][2];
+        float2 x[NG][2][NH];
         q.logits(x, ring, st, live);
-        uint32_t ent[NT / 2][4];
-        float mx[2], big = 0.f;
+        uint32_t ent[NG][2];
+        float2 mx[NH];
+        float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) {
-            ring.entries(ent[i], st, i, true);
-#pragma unroll
-            for (int je = 0; je < 4; je += 2)
-                big = tc::max3f(big, fabsf(entry_scale(ent[i][je])), fabsf(entry_scale(ent[i][je + 1])));
+        for (int i = 0; i < NG; ++i) {
+            ent[i][0] = ring.entry(st, i, 0, true);
+            ent[i][1] = ring.entry(st, i, 1, true);
+            big = tc::max3f(big, fabsf(entry_scale(ent[i][0])), fabsf(entry_scale(ent[i][1])));
         }
+        bool grow = big > up;
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            mx[hr] = fmaxf(x[0][hr].x, x[0][hr].y);
-#pragma unroll
-            for (int j = 1; j < NT; ++j) mx[hr] = tc::max3f(mx[hr], x[j][hr].x, x[j][hr].y);
-            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
-            mx[hr] *= q.kf[hr];
+        for (int n = 0; n < NH; ++n) {
+            float2 v = x[0][0][n];
+            if constexpr (NG == 2) {
+                v.x = fmaxf(tc::max3f(v.x, x[0][1][n].x, x[1][0][n].x), x[1][1][n].x);
+                v.y = fmaxf(tc::max3f(v.y, x[0][1][n].y, x[1][0][n].y), x[1][1][n].y);
+            } else {
+                v.x = fmaxf(v.x, x[0][1][n].x);
+                v.y = fmaxf(v.y, x[0][1][n].y);
+            }
+            mx[n] = fmul2(v, q.kf[n]);
+            grow |= mx[n].x > m[n].x + 14.f || mx[n].y > m[n].y + 14.f;
         }
-        maxima(at, mx[0], mx[1]);
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + 14.f || mx[1] > m[1] + 14.f || big > up))
-            rescale(mx[0], mx[1], big);
+        maxima(at, mx);
+        if (__any_sync(0xffffffffu, grow)) rescale(mx, big);
         const float down = up == 0.f ? 0.f : __uint_as_float(0x7f000000u - __float_as_uint(up));
-        const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+        float2 nm[NH];
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) {
-            uint32_t a[4];
+        for (int n = 0; n < NH; ++n)
+            nm[n] = make_float2(m[n].x == -INFINITY ? 0.f : -m[n].x,
+                                m[n].y == -INFINITY ? 0.f : -m[n].y);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                float2 sc, z;
-                entry_pair(ent[i][2 * jj], ent[i][2 * jj + 1], sc, z);
-                sc = fmul2(sc, both(down));
+        for (int i = 0; i < NG; ++i) {
+            uint32_t b[NH][2];
 #pragma unroll
-                for (int hr = 0; hr < 2; ++hr) {
-                    const float2 y = tc::ffma2(x[2 * i + jj][hr], both(q.kf[hr]), both(nm[hr]));
+            for (int k = 0; k < 2; ++k) {
+                const float2 z = both(entry_zero(ent[i][k]));
+                const float2 sd = both(entry_scale(ent[i][k]) * down);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    const float2 y = tc::ffma2(x[i][k][n], q.kf[n], nm[n]);
                     const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                    l[hr] = tc::fadd2(l[hr], p);
-                    zacc[hr] = tc::ffma2(p, z, zacc[hr]);
-                    const float2 w = fmul2(p, sc);
-                    a[2 * jj + hr] = pack_f16(w.x, w.y);
+                    l[n] = tc::fadd2(l[n], p);
+                    zacc[n] = tc::ffma2(p, z, zacc[n]);
+                    const float2 w = fmul2(p, sd);
+                    b[n][k] = transpose8(pack_f16(w.x, w.y));
                 }
             }
             uint32_t v[4][Ring::R::kVW];
@@ -565,11 +614,16 @@ struct QAttend {
             for (int je = 0; je < 4; ++je) ring.v_words(v[je], st, i, je);
 #pragma unroll
             for (int j = 0; j < D / 8; j += 4) {
-                uint32_t b0[4], b1[4];
-                v_pairs<F>(v[0], v[1], j, b0);
-                v_pairs<F>(v[2], v[3], j, b1);
+                uint32_t p0[4], p1[4];
+                v_pairs<F>(v[0], v[1], j, p0);
+                v_pairs<F>(v[2], v[3], j, p1);
+                const uint32_t a0[4] = {p0[0], p0[1], p1[0], p1[1]};
+                const uint32_t a1[4] = {p0[2], p0[3], p1[2], p1[3]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma_f16(o[j + e], a, b0[e], b1[e]);
+                for (int n = 0; n < NH; ++n) {
+                    mma_f16(o[j / 2][n], a0, b[n][0], b[n][1]);
+                    mma_f16(o[j / 2 + 1][n], a1, b[n][0], b[n][1]);
+                }
             }
         }
     }
@@ -609,48 +663,51 @@ struct QAttend {
         __syncwarp();  // the ring may be reused
     }
 
-    // Sums over the quad, puts O in its own units and adds the zero points:
-    // o = sum p v^, l[hr].x = sum p.
+    // Sums over the warp, puts O in its own units and adds the zero points:
+    // o = sum p v^, l = sum p.
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            float s = l[hr].x + l[hr].y, z = zacc[hr].x + zacc[hr].y;
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            z += __shfl_xor_sync(0xffffffffu, z, 1);
-            z += __shfl_xor_sync(0xffffffffu, z, 2);
-            l[hr].x = s;
+        for (int n = 0; n < NH; ++n) {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                o[j][2 * hr] = fmaf(o[j][2 * hr], up / kCodeUnit<F>, z);
-                o[j][2 * hr + 1] = fmaf(o[j][2 * hr + 1], up / kCodeUnit<F>, z);
+            for (int w = 4; w < 32; w <<= 1) {
+                l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, w);
+                l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, w);
+                zacc[n].x += __shfl_xor_sync(0xffffffffu, zacc[n].x, w);
+                zacc[n].y += __shfl_xor_sync(0xffffffffu, zacc[n].y, w);
             }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[j][n][e] = fmaf(o[j][n][e], up / kCodeUnit<F>, e & 1 ? zacc[n].y : zacc[n].x);
         }
     }
 
-    // Partial (after finish): part[2 h] = m, part[2 h + 1] = l, then O rows of D
-    // floats at part + 32 (16 heads).
+    // After finish, of head 8 n + 2 t + e: the lane's D / 8 dimensions from gid D / 8 on.
+    __device__ __forceinline__ float dim(int n, int e, int x) const { return o[x >> 1][n][2 * (x & 1) + e]; }
+    static constexpr int kPart = 32 + 16 * D;  // floats of a partial
+
+    // Partial: part[2 h] = m, part[2 h + 1] = l, then O rows of D floats at part + 32
+    // (16 heads).
     __device__ __forceinline__ void store_part(float* part, int g) const {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            const int h = gid + 8 * hr;
-            if (h >= g) continue;
-            if (t == 0) {
-                part[2 * h] = m[hr];
-                part[2 * h + 1] = l[hr].x;
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * n + 2 * t + e;
+                if (h >= g) continue;
+                if (gid == 0) {
+                    part[2 * h] = e ? m[n].y : m[n].x;
+                    part[2 * h + 1] = e ? l[n].y : l[n].x;
+                }
+                float* row = part + 32 + h * D + gid * (D / 8);
+#pragma unroll
+                for (int x = 0; x < D / 8; x += 4)
+                    *reinterpret_cast<float4*>(row + x) = make_float4(
+                        dim(n, e, x), dim(n, e, x + 1), dim(n, e, x + 2), dim(n, e, x + 3));
             }
-            float* row = part + 32 + h * D + t * (D / 4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int j = 0; j < D / 8; j += 4)
-                    *reinterpret_cast<float4*>(row + e * (D / 8) + j) =
-                        make_float4(o[j][2 * hr + e], o[j + 1][2 * hr + e], o[j + 2][2 * hr + e],
-                                    o[j + 3][2 * hr + e]);
-        }
     }
-    static constexpr int kPart = 32 + 16 * D;  // floats of a partial
 };
 
 // Bases of unit (b, u): a contiguous cache's rows of that unit, or the pool.

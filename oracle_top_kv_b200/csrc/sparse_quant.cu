@@ -4,7 +4,7 @@
 // thread-block cluster per (sequence, KV group); the unit's rows are dealt to
 // its warps in steps, partials are merged per CTA in shared memory and over
 // the cluster in distributed shared memory.
-#include <atomic>
+#include <type_traits>
 
 #include "hs_common.cuh"
 #include "hs_kernels.cuh"
@@ -15,39 +15,47 @@ namespace sq {
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
-template <int D, int F> using Attend = QAttend<D, F, kStages>;
-template <int D, int F>
-constexpr size_t kRingBytes = (size_t)kWarps * Attend<D, F>::Ring::kBytes;
+// 16 heads: Q in shared memory lets three CTAs share an SM without spills (2048 rows x 4
+// groups x 1024 keys: XXX us against YYY with Q in registers).
+template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2>;
+template <int D, int F, int NH>
+constexpr size_t kRingBytes =  // the warps' rings, then their queries
+    (size_t)kWarps * (QRing<D, F, true, kStages>::kBytes + QQuery<D, F, NH, NH == 2>::kBytes);
+// Four-warp CTAs to an SM that the registers are divided for.
+template <int NH> constexpr int kPerSm = NH == 1 ? 4 : 3;
 
 // Writes a unit's heads from a warp's finished accumulators.
-template <int D, class A>
+template <int D, int NH, class A>
 __device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o, float* lse,
                                            size_t head0, size_t stride) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-        const int h = gid + 8 * hr;
-        if (h >= g) continue;
-        const float inv = st.l[hr].x == 0.f ? 0.f : 1.f / st.l[hr].x;
-        const size_t row = head0 + h * stride;
-        __nv_bfloat16* dst = o + row * D + t * (D / 4);
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+            const int h = 8 * n + 2 * t + e;
+            if (h >= g) continue;
+            const float l = e ? st.l[n].y : st.l[n].x;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t row = head0 + h * stride;
+            __nv_bfloat16* dst = o + row * D + gid * (D / 8);
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 8) {
+            for (int x = 0; x < D / 8; x += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w[i] = pack_bf16(st.o[j + 2 * i][2 * hr + e] * inv,
-                                     st.o[j + 2 * i + 1][2 * hr + e] * inv);
-                *reinterpret_cast<uint4*>(dst + e * (D / 8) + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    w[i] = pack_bf16(st.dim(n, e, x + 2 * i) * inv, st.dim(n, e, x + 2 * i + 1) * inv);
+                *reinterpret_cast<uint4*>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-        if (t == 0) lse[row] = st.l[hr].x == 0.f ? -INFINITY : (st.m[hr] + log2f(st.l[hr].x)) * kLn2;
-    }
+            if (gid == 0) {
+                const float m = e ? st.m[n].y : st.m[n].x;
+                lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            }
+        }
 }
 
-template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+template <int D, int F, int NH>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                         const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
                         __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
@@ -58,16 +66,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int u = unit % p.hkv, b = unit / p.hkv;
     const size_t head0 = ((size_t)b * p.hq + (size_t)u * p.group) * p.t_q + j;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    using A = Attend<D, F>;
+    using A = Attend<D, F, NH>;
     const typename A::Ring ring{smem_u32(smem_raw) + (threadIdx.x >> 5) * A::Ring::kBytes};
     A st;
-    st.init(q + head0 * D, (size_t)p.t_q * D, p.group, p.scale_log2);
+    st.init(q + head0 * D, (size_t)p.t_q * D, p.group, p.scale_log2,
+            smem_u32(smem_raw) + kWarps * A::Ring::kBytes + (threadIdx.x >> 5) * decltype(st.q)::kBytes);
     const int n = clamp_count(cnt[task], p.ksel) * p.block_size;
     const QIndex src{idx + (size_t)task * p.ksel, n,           p.block_size,
                      p.q_offset + j,              p.bt != nullptr, page_map(p, b, u)};
     st.run(ring, unit_cache<D, F>(p, cache, unit), src, 0, 1, (n + A::NK - 1) / A::NK, NoMaxima{});
     st.finish();
-    store_rows<D>(st, p.group, o, lse, head0, (size_t)p.t_q);
+    store_rows<D, NH>(st, p.group, o, lse, head0, (size_t)p.t_q);
 }
 
 // Weight of a partial with reference m under the common reference M.
@@ -75,14 +84,14 @@ __device__ __forceinline__ float merge_weight(float m, float M) {
     return m == -INFINITY ? 0.f : exp2f(m - M);
 }
 
-template <int D, int F>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+template <int D, int F, int NH>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     decode_sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                                const int32_t* __restrict__ seq_len,
                                const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
                                int csize, __nv_bfloat16* __restrict__ o,
                                float* __restrict__ lse) {
-    using A = Attend<D, F>;
+    using A = Attend<D, F, NH>;
     // the warps' rings, reused for their partials; then the CTA's partial
     extern __shared__ __align__(16) unsigned char smem_raw[];
     constexpr int kStride = A::Ring::kBytes / 4;  // floats between the warps' partials
@@ -96,7 +105,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const bool valid = L >= 1 && L <= p.t_kv;
     const size_t head0 = (size_t)b * p.hq + (size_t)u * g;
     A st;
-    st.init(q + head0 * D, D, g, p.scale_log2);
+    st.init(q + head0 * D, D, g, p.scale_log2,
+            smem_u32(smem_raw) + kWarps * A::Ring::kBytes + warp * decltype(st.q)::kBytes);
     const typename A::Ring ring{smem_u32(smem_raw) + warp * A::Ring::kBytes};
     if (valid) {
         const int n = clamp_count(cnt[unit], p.ksel);
@@ -111,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     st.store_part(smem + warp * kStride, g);
     __syncthreads();
     // the CTA's partial
-    float* mine = smem + kWarps * kStride;
+    float* mine = smem + kRingBytes<D, F, NH> / sizeof(float);
     for (int e = threadIdx.x; e < g * D; e += blockDim.x) {
         const int h = e / D;
         float M = -INFINITY, l = 0.f, acc = 0.f;
@@ -151,26 +161,26 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     if (csize > 1) cluster_sync_all();  // peers keep their shared memory until all have read
 }
 
-template <int D, int F>
+template <int D, int F, int NH>
 static cudaError_t launch_sparse_t(const KParams& p, const QuantCache& c, const void* q,
                                    const int32_t* idx, const int32_t* cnt, void* o, float* lse,
                                    cudaStream_t st) {
     const long long tasks = (long long)p.batch * p.hkv * p.t_q;
-    auto kern = sparse_quant_kernel<D, F>;
+    auto kern = sparse_quant_kernel<D, F, NH>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)kRingBytes<D, F>);
+                                               (int)kRingBytes<D, F, NH>);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, kRingBytes<D, F>, st>>>(
+    kern<<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, kRingBytes<D, F, NH>, st>>>(
         p, c, (const __nv_bfloat16*)q, idx, cnt, (__nv_bfloat16*)o, lse);
     return cudaGetLastError();
 }
 
-template <int D, int F>
+template <int D, int F, int NH>
 static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const void* q,
                                    const int32_t* seq_len, const int32_t* idx, const int32_t* cnt,
                                    void* o, float* lse, cudaStream_t st) {
-    auto kern = decode_sparse_quant_kernel<D, F>;
-    const size_t smem = kRingBytes<D, F> + Attend<D, F>::kPart * sizeof(float);
+    auto kern = decode_sparse_quant_kernel<D, F, NH>;
+    const size_t smem = kRingBytes<D, F, NH> + Attend<D, F, NH>::kPart * sizeof(float);
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -181,7 +191,7 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
     // Widest cluster (a portable size) whose CTAs still run in one wave, two
     // to an SM, with a step for every warp.
     const int units = p.batch * p.hkv;
-    const int steps = (p.ksel + Attend<D, F>::NK - 1) / Attend<D, F>::NK;
+    const int steps = (p.ksel + Attend<D, F, NH>::NK - 1) / Attend<D, F, NH>::NK;
     int csize = 1;
     while (csize < 8 && units * csize * 2 <= 2 * sms && kWarps * csize < steps) csize *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -200,28 +210,48 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
                               (__nv_bfloat16*)o, lse);
 }
 
+// Calls fn.operator()<D, F, NH>(): NH 8-head tiles hold the group.
+template <typename Fn>
+static cudaError_t dispatch(const KParams& p, int format, Fn fn) {
+    auto by_g = [&](auto d, auto f) {
+        constexpr int D = decltype(d)::value, F = decltype(f)::value;
+        return p.group <= 8 ? fn.template operator()<D, F, 1>() : fn.template operator()<D, F, 2>();
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    using F4 = std::integral_constant<int, HS_KV_INT4>;
+    using F8 = std::integral_constant<int, HS_KV_FP8>;
+    if (format == HS_KV_INT4) return p.head_dim == 64 ? by_g(I64{}, F4{}) : by_g(I128{}, F4{});
+    return p.head_dim == 64 ? by_g(I64{}, F8{}) : by_g(I128{}, F8{});
+}
+
+struct SparseLaunch {
+    const KParams& p;
+    const QuantCache& c;
+    const void* q;
+    const int32_t *seq_len, *idx, *cnt;  // seq_len: a decode step
+    void* o;
+    float* lse;
+    cudaStream_t st;
+    template <int D, int F, int NH>
+    cudaError_t operator()() const {
+        return seq_len ? launch_decode_t<D, F, NH>(p, c, q, seq_len, idx, cnt, o, lse, st)
+                       : launch_sparse_t<D, F, NH>(p, c, q, idx, cnt, o, lse, st);
+    }
+};
+
 }  // namespace sq
 
 cudaError_t launch_sparse_quant(const KParams& p, int format, const QuantCache& c, const void* q,
                                 const int32_t* idx, const int32_t* cnt, void* o, float* lse,
                                 cudaStream_t st) {
-    if (format == HS_KV_INT4)
-        return p.head_dim == 64 ? sq::launch_sparse_t<64, HS_KV_INT4>(p, c, q, idx, cnt, o, lse, st)
-                                : sq::launch_sparse_t<128, HS_KV_INT4>(p, c, q, idx, cnt, o, lse, st);
-    return p.head_dim == 64 ? sq::launch_sparse_t<64, HS_KV_FP8>(p, c, q, idx, cnt, o, lse, st)
-                            : sq::launch_sparse_t<128, HS_KV_FP8>(p, c, q, idx, cnt, o, lse, st);
+    return sq::dispatch(p, format, sq::SparseLaunch{p, c, q, nullptr, idx, cnt, o, lse, st});
 }
 
 cudaError_t launch_decode_sparse_quant(const KParams& p, int format, const QuantCache& c,
                                        const void* q, const int32_t* seq_len, const int32_t* idx,
                                        const int32_t* cnt, void* o, float* lse, cudaStream_t st) {
-    if (format == HS_KV_INT4)
-        return p.head_dim == 64
-                   ? sq::launch_decode_t<64, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, st)
-                   : sq::launch_decode_t<128, HS_KV_INT4>(p, c, q, seq_len, idx, cnt, o, lse, st);
-    return p.head_dim == 64
-               ? sq::launch_decode_t<64, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, st)
-               : sq::launch_decode_t<128, HS_KV_FP8>(p, c, q, seq_len, idx, cnt, o, lse, st);
+    return sq::dispatch(p, format, sq::SparseLaunch{p, c, q, seq_len, idx, cnt, o, lse, st});
 }
 
 }  // namespace hs

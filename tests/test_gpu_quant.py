@@ -241,6 +241,8 @@ DECODE = [
     (1, 16, 1, 128, 40000, 1024, 128, 0, [39999]),        # many slices
     (1, 4, 1, 128, 20000, 1500, 100, 0, [20000]),         # k - w > 1024
     (5, 7, 7, 128, 100, 300, 10, 0, [1, 31, 32, 33, 100]),  # everything selected, groups of one
+    (1, 16, 1, 64, 9000, 4096, 0, 0, [9000]),               # the largest budget, no window
+    (2, 3, 1, 128, 70000, 64, 16, 16, [70000, 66001]),      # units on clusters, small group
     (40, 4, 2, 64, 96, 16, 4, 16, [(7 * i) % 96 + 1 for i in range(40)]),
 ]
 
