@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
         const QuantCache uc = unit_cache<D, F>(p, cache, unit);
         const int L = __ldg(seq_len + b);
         const TileMaxima tm{ws.tmax + (size_t)unit * ws.tiles * 16};
-        if (p.bt) st.run(ring, uc, QPagedRange{0, L, page_map(p, b, u)}, s0 + warp, kWarps, s1, tm);
-        else st.run(ring, uc, QRange{0, L}, s0 + warp, kWarps, s1, tm);
+        if (p.bt) st.run(ring, uc, QPagedRange{L, page_map(p, b, u)}, s0 + warp, kWarps, s1, tm);
+        else st.template run_dense<kWarps>(ring, uc, L, s0 + warp, s1, tm);
         st.finish();
         st.store_part(smem + warp * kStride, g);
         __syncthreads();
@@ -320,22 +320,23 @@ __device__ uint64_t cluster_kth_largest(Get get, int n, int k, CtaSelectSmem& sh
 // tile), keys below `end` only.
 template <int NK>
 struct QTiles {
-    static constexpr bool kDirect = false;
     const int* tiles;
     int n_tiles, end;
     bool paged;
     PageMap pm;
-    __device__ __forceinline__ int key(int slot) const {
-        return slot < n_tiles * NK ? tiles[slot / NK] * NK + slot % NK : end;
-    }
+    __device__ __forceinline__ int key(int slot) const { return tiles[slot / NK] * NK + slot % NK; }
     __device__ __forceinline__ int row(int slot) const {
         const int k = key(slot);
         return k >= end ? -1 : paged ? pm.row(k) : k;
     }
+    __device__ __forceinline__ int run(int slot, int N) const {
+        const int k = key(slot);
+        if (k + N > end || (paged && pm.page_size % N)) return -1;
+        return paged ? pm.row(k) : k;
+    }
 };
-// The same of consecutive keys first ...
+// Consecutive keys first .. end - 1.
 struct QKeys {
-    static constexpr bool kDirect = false;
     int first, end;
     bool paged;
     PageMap pm;
@@ -344,6 +345,7 @@ struct QKeys {
         const int k = first + slot;
         return k >= end ? -1 : paged ? pm.row(k) : k;
     }
+    __device__ __forceinline__ int run(int, int) const { return -1; }
 };
 
 // Rescores a source's keys, warp w of the CTA steps w, w + kSelWarps, ...: put(key,
@@ -356,26 +358,26 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F, NH>& q, const floa
     constexpr int NK = Ring::NK;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
     const Ring ring{ring_base + warp * Ring::kBytes};
-    auto mine = [&](int st) { return st < n_steps ? src.row(st * NK + (lane & (NK - 1))) : -1; };
-    int row = mine(warp), ahead = warp;
+    int ahead = warp;
+    QPlace at = place_of<NK>(src, ahead, n_steps);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (ahead < n_steps) ring.fill(i, c, src, ahead * NK, row);
+        if (ahead < n_steps) ring.fill(i, c, at);
         cp_async_commit();
         ahead += kSelWarps;
-        row = mine(ahead);
+        at = place_of<NK>(src, ahead, n_steps);
     }
     int s = 0, rounds = 0;
     for (int r0 = 0; r0 < n_steps; r0 += kSelWarps) {
         const int st = r0 + warp;
         cp_async_wait<1>();
         __syncwarp();
-        if (ahead < n_steps) ring.fill(s == 0 ? 2 : s - 1, c, src, ahead * NK, row);
+        if (ahead < n_steps) ring.fill(s == 0 ? 2 : s - 1, c, at);
         cp_async_commit();
         ahead += kSelWarps;
-        row = mine(ahead);
+        at = place_of<NK>(src, ahead, n_steps);
         if (st < n_steps) {
-            const uint32_t live = ring.live(s, src, st * NK);
+            const uint32_t live = ring.live(s);
             float2 x[NK / 16][2][NH];
             q.logits(x, ring, ring.stage(s), live);
 #pragma unroll

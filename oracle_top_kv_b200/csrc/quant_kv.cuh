@@ -130,26 +130,21 @@ __device__ __forceinline__ void v_pairs(const uint32_t (&a)[N], const uint32_t (
 // ------------------------------------------------------------- row sources
 // row(slot) = row, relative to the bases handed to the warp, of key slot
 // 0..n-1 of its list, -1 if that slot is masked or out of range.
+// run(slot, N) = row of `slot` if the N slots from there (a multiple of N) all count and
+// lie in consecutive rows, else -1 (the caller then asks for each).
 
-// Consecutive rows first + slot of a contiguous cache.
-struct QRange {
-    static constexpr bool kDirect = true;  // cheap: each lane asks for what it loads
-    int first, n;
-    __device__ __forceinline__ int row(int slot) const { return slot < n ? first + slot : -1; }
-};
-// Logical keys first + slot through the block table.
+// Logical keys 0 .. n - 1 through the block table.
 struct QPagedRange {
-    static constexpr bool kDirect = false;
-    int first, n;
+    int n;
     PageMap pm;
-    __device__ __forceinline__ int row(int slot) const {
-        return slot < n ? pm.row(first + slot) : -1;
+    __device__ __forceinline__ int row(int slot) const { return slot < n ? pm.row(slot) : -1; }
+    __device__ __forceinline__ int run(int slot, int N) const {
+        return slot + N > n || pm.page_size % N ? -1 : pm.row(slot);
     }
 };
 // Entries of an index row (token mode: keys; block mode: blocks clipped to
 // keys <= t), through the block table if there is one.
 struct QIndex {
-    static constexpr bool kDirect = false;
     const int32_t* ids;
     int n, B, t;
     bool paged;
@@ -169,7 +164,28 @@ struct QIndex {
         }
         return paged ? pm.row(key) : key;
     }
+    __device__ __forceinline__ int run(int slot, int N) const {
+        if (B % N || slot + N > n || (paged && pm.page_size % N)) return -1;
+        const int jb = slot / B;
+        const int id = __ldg(ids + jb);
+        if (id < 0 || id > t / B) return -1;  // row() reports it
+        const int key = id * B + (slot - jb * B);
+        if (key + N - 1 > t) return -1;
+        return paged ? pm.row(key) : key;
+    }
 };
+// The place of a step of NK slots: a run's first row, or this lane's row (lane % NK).
+struct QPlace {
+    int row;
+    bool run;
+};
+template <int NK, class Src>
+__device__ __forceinline__ QPlace place_of(const Src& src, int step, int n_steps) {
+    if (step >= n_steps) return QPlace{-1, false};
+    const int r = src.run(step * NK, NK);
+    if (r >= 0) return QPlace{r, true};
+    return QPlace{src.row(step * NK + (int)(threadIdx.x & (NK - 1))), false};
+}
 
 // -------------------------------------------------------------- ring of rows
 // A warp's stages.  K only: the V half is neither filled nor reserved.
@@ -218,61 +234,82 @@ struct QRing {
         else return k_to + (uint32_t)i * 512u;
     }
 
-    // Starts the copies of the step whose first slot is slot0.  `mine`: row of
-    // slot slot0 + lane % NK, for sources that are not direct.
-    template <class Src>
-    __device__ __forceinline__ void fill(int s, const QuantCache& c, const Src& src, int slot0,
-                                         int mine) const {
+    // Starts the copies of a step.
+    __device__ __forceinline__ void fill(int s, const QuantCache& c, const QPlace& at) const {
         const int lane = threadIdx.x & 31;
         const uint32_t st = stage(s);
-        if constexpr (Src::kDirect) {
-            const int r0 = src.first + slot0;
-            if (slot0 + NK <= src.n) {  // a whole step: consecutive bytes
-                const uint8_t* kp = c.kc + (size_t)r0 * RB + lane * 16;
-                const uint8_t* vp = c.vc + (size_t)r0 * RB + lane * 16;
-#pragma unroll
-                for (int i = 0; i < NK / PASS; ++i) {
-                    copy16(st + k_dst(i), kp + i * 512);
-                    if constexpr (kV) copy16(st + v_to + i * 512, vp + i * 512);
-                }
-                if (NK == 32 || lane < NK) {
-                    copy4(st + e_to, c.ks + (size_t)r0 + lane);
-                    if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (size_t)r0 + lane);
-                }
-                return;
-            }
-            mine = src.row(slot0 + (lane & (NK - 1)));
-        }
-        const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
-        if (live == 0xffffffffu) {
+        uint32_t live = 0xffffffffu;
+        if (at.run) {  // consecutive bytes
+            const uint8_t* kp = c.kc + (size_t)at.row * RB + lane * 16;
+            const uint8_t* vp = c.vc + (size_t)at.row * RB + lane * 16;
 #pragma unroll
             for (int i = 0; i < NK / PASS; ++i) {
-                const uint32_t r = __shfl_sync(0xffffffffu, mine, lane / CH + i * PASS);
+                copy16(st + k_dst(i), kp + i * 512);
+                if constexpr (kV) copy16(st + v_to + i * 512, vp + i * 512);
+            }
+            if (NK == 32 || lane < NK) {
+                copy4(st + e_to, c.ks + (size_t)at.row + lane);
+                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (size_t)at.row + lane);
+            }
+        } else if ((live = __ballot_sync(0xffffffffu, at.row >= 0)) == 0xffffffffu) {
+#pragma unroll
+            for (int i = 0; i < NK / PASS; ++i) {
+                const uint32_t r = __shfl_sync(0xffffffffu, at.row, lane / CH + i * PASS);
                 const size_t off = (size_t)r * RB + (lane % CH) * 16;
                 copy16(st + k_dst(i), c.kc + off);
                 if constexpr (kV) copy16(st + v_to + i * 512, c.vc + off);
             }
             if (NK == 32 || lane < NK) {
-                copy4(st + e_to, c.ks + (uint32_t)mine);
-                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (uint32_t)mine);
+                copy4(st + e_to, c.ks + (uint32_t)at.row);
+                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (uint32_t)at.row);
             }
         } else {  // rows that do not count are zeros
 #pragma unroll
             for (int i = 0; i < NK / PASS; ++i) {
-                const int r = __shfl_sync(0xffffffffu, mine, lane / CH + i * PASS);
+                const int r = __shfl_sync(0xffffffffu, at.row, lane / CH + i * PASS);
                 const size_t off = r >= 0 ? (size_t)r * RB + (lane % CH) * 16 : 0;
                 cp_async16(st + k_dst(i), c.kc + off, r >= 0);
                 if constexpr (kV) cp_async16(st + v_to + i * 512, c.vc + off, r >= 0);
             }
             if (NK == 32 || lane < NK) {
-                const size_t off = mine >= 0 ? (size_t)mine : 0;
-                cp_async4(st + e_to, c.ks + off, mine >= 0);
-                if constexpr (kV) cp_async4(st + kHalf + e_to, c.vs + off, mine >= 0);
+                const size_t off = at.row >= 0 ? (size_t)at.row : 0;
+                cp_async4(st + e_to, c.ks + off, at.row >= 0);
+                if constexpr (kV) cp_async4(st + kHalf + e_to, c.vs + off, at.row >= 0);
             }
         }
-        if constexpr (!Src::kDirect) {
-            if (lane == 0)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(mask_at(s)), "r"(live) : "memory");
+        if (lane == 0)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(mask_at(s)), "r"(live) : "memory");
+    }
+    // The same of NK consecutive rows, given the lane's 16 bytes and entry of the first
+    // rows; `to`: offset of the stage.
+    __device__ __forceinline__ void fill_dense(uint32_t to, const uint8_t* kp, const uint8_t* vp,
+                                               const uint32_t* ke, const uint32_t* ve) const {
+        const uint32_t st = base + to;
+#pragma unroll
+        for (int i = 0; i < NK / PASS; ++i) {
+            copy16(st + k_dst(i), kp + i * 512);
+            if constexpr (kV) copy16(st + v_to + i * 512, vp + i * 512);
+        }
+        if (NK == 32 || (threadIdx.x & 31) < NK) {
+            copy4(st + e_to, ke);
+            if constexpr (kV) copy4(st + kHalf + e_to, ve);
+        }
+    }
+    // Only the rows that exist: `left` rows from row number `lane` of the step on.
+    __device__ __forceinline__ void fill_tail(uint32_t to, const uint8_t* kp, const uint8_t* vp,
+                                              const uint32_t* ke, const uint32_t* ve,
+                                              int left) const {
+        const uint32_t st = base + to;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < NK / PASS; ++i) {
+            const bool ok = lane / CH + i * PASS < left + lane;
+            cp_async16(st + k_dst(i), ok ? kp + i * 512 : kp, ok);
+            if constexpr (kV) cp_async16(st + v_to + i * 512, ok ? vp + i * 512 : vp, ok);
+        }
+        if (NK == 32 || lane < NK) {
+            cp_async4(st + e_to, ke, left > 0);
+            if constexpr (kV) cp_async4(st + kHalf + e_to, ve, left > 0);
         }
     }
     __device__ static __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -286,18 +323,11 @@ struct QRing {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n));
     }
 
-    // Bit x: slot slot0 + x counts (x < NK).
-    template <class Src>
-    __device__ __forceinline__ uint32_t live(int s, const Src& src, int slot0) const {
-        constexpr uint32_t kAll = NK == 32 ? 0xffffffffu : 0xffffu;
-        if constexpr (Src::kDirect) {
-            const int left = src.n - slot0;
-            return left >= NK ? kAll : (1u << max(left, 0)) - 1u;
-        } else {
-            uint32_t m;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(mask_at(s)) : "memory");
-            return m & kAll;
-        }
+    // Bit x: slot x of the stage counts (x < NK).
+    __device__ __forceinline__ uint32_t live(int s) const {
+        uint32_t m;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m) : "r"(mask_at(s)) : "memory");
+        return m & (NK == 32 ? 0xffffffffu : 0xffffu);
     }
 
     template <int N>
@@ -632,35 +662,72 @@ struct QAttend {
     template <class Src, class Maxima>
     __device__ __forceinline__ void run(const Ring& ring, const QuantCache& c, const Src& src,
                                         int first, int stride, int n_steps, const Maxima& maxima) {
-        const int lane = threadIdx.x & 31;
-        auto mine = [&](int st) {
-            if constexpr (Src::kDirect) return 0;
-            else return st < n_steps ? src.row(st * NK + (lane & (NK - 1))) : -1;
-        };
         // copies run kStages - 1 steps ahead, the rows' places one more
         int ahead = first;
-        int row = mine(first);
+        QPlace at = place_of<NK>(src, ahead, n_steps);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            if (ahead < n_steps) ring.fill(i, c, src, ahead * NK, row);
+            if (ahead < n_steps) ring.fill(i, c, at);
             cp_async_commit();
             ahead += stride;
-            row = mine(ahead);
+            at = place_of<NK>(src, ahead, n_steps);
         }
         int s = 0, fs = kStages - 1;
         for (int st = first; st < n_steps; st += stride) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            if (ahead < n_steps) ring.fill(fs, c, src, ahead * NK, row);
+            if (ahead < n_steps) ring.fill(fs, c, at);
             cp_async_commit();
             ahead += stride;
-            row = mine(ahead);
-            step(ring, ring.stage(s), ring.live(s, src, st * NK), st, maxima);
+            at = place_of<NK>(src, ahead, n_steps);
+            step(ring, ring.stage(s), ring.live(s), st, maxima);
             s = s + 1 == kStages ? 0 : s + 1;
             fs = fs + 1 == kStages ? 0 : fs + 1;
         }
         cp_async_wait<0>();
         __syncwarp();  // the ring may be reused
+    }
+
+    // The same for rows 0 .. n - 1 of the bases, kStride steps apart: running pointers in
+    // place of row numbers (a hundred cycles of 1400 a step, at 16 heads of 128).
+    template <int kStride, class Maxima>
+    __device__ __forceinline__ void run_dense(const Ring& ring, const QuantCache& c, int n,
+                                              int first, int n_steps, const Maxima& maxima) {
+        const int lane = threadIdx.x & 31;
+        constexpr uint32_t kRow = kStride * NK, kEnd = kStages * Ring::kStage;
+        const size_t r0 = (size_t)first * NK;
+        const uint8_t* kp = c.kc + r0 * Ring::RB + lane * 16;
+        const uint8_t* vp = c.vc + r0 * Ring::RB + lane * 16;
+        const uint32_t *ke = c.ks + r0 + lane, *ve = c.vs + r0 + lane;
+        int ahead = first;
+        uint32_t to = 0, at = 0;  // stages' offsets: filled next, read next
+        auto fill = [&] {
+            if (ahead < n_steps) {
+                const int left = n - ahead * NK - lane;  // keys from the lane's on
+                if ((ahead + 1) * NK <= n) ring.fill_dense(to, kp, vp, ke, ve);
+                else ring.fill_tail(to, kp, vp, ke, ve, left);
+                kp += kRow * Ring::RB;
+                vp += kRow * Ring::RB;
+                ke += kRow;
+                ve += kRow;
+            }
+            cp_async_commit();
+            ahead += kStride;
+            to = to + Ring::kStage == kEnd ? 0u : to + Ring::kStage;
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fill();
+        for (int st = first; st < n_steps; st += kStride) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            fill();
+            const int left = n - st * NK;
+            const uint32_t live = left >= NK ? (NK == 32 ? 0xffffffffu : 0xffffu) : (1u << left) - 1u;
+            step(ring, ring.base + at, live, st, maxima);
+            at = at + Ring::kStage == kEnd ? 0u : at + Ring::kStage;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
     }
 
     // Sums over the warp, puts O in its own units and adds the zero points:
