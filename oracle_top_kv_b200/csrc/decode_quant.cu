@@ -29,7 +29,7 @@ namespace hs {
 namespace dq {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMaxCtas = 640;  // partial slots reserved: at most kMaxCtas + units
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages>;
 // Four-warp CTAs of the full kernel to an SM that the registers are divided for.

@@ -331,7 +331,6 @@ hs_status quant_rows(const hs_params* p, const hs_kv_quant* kv, const hs_pages* 
     hs_status s = resolve_quant(p, kv, pages, false, &kp, &c);
     if (s != HS_OK) return s;
     if (!ok_ptr(k) || !ok_ptr(v) || !ok_opt(seq_len) || !ok_opt(n_new)) return HS_ERR_INVALID_ARG;
-    if (!hs::kv_quant_supported(kp)) return HS_ERR_INVALID_ARG;
     if (kp.t_q == 0) return HS_OK;
     return launched(1, [&] {
         return hs::launch_kv_quant(kp, p->dtype, kv->format, kv->k_codes, kv->k_scale,

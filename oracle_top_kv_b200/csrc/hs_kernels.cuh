@@ -122,7 +122,6 @@ cudaError_t launch_token_select_wide(const KParams& p, const void* q, const void
 // Quantised K^F/V^F (format: hs_kv_format; d = 64 or 128, groups of up to 16
 // heads): rows written and read back, and the attention steps over them.
 struct QuantCache;
-bool kv_quant_supported(const KParams& p);
 cudaError_t launch_kv_quant(const KParams& p, int dtype, int format, void* k_codes, void* k_entry,
                             void* v_codes, void* v_entry, void* k, void* v,
                             const int32_t* seq_len, const int32_t* n_new, bool write,

@@ -147,7 +147,7 @@ struct QPagedRange {
 struct QIndex {
     const int32_t* ids;
     int n, B, t;
-    bool paged;
+    bool paged, runs;  // runs: every NK slots from a multiple of NK may be consecutive rows
     PageMap pm;
     __device__ __forceinline__ int row(int slot) const {
         if (slot >= n) return -1;
@@ -165,7 +165,7 @@ struct QIndex {
         return paged ? pm.row(key) : key;
     }
     __device__ __forceinline__ int run(int slot, int N) const {
-        if (B % N || slot + N > n || (paged && pm.page_size % N)) return -1;
+        if (!runs || slot + N > n) return -1;
         const int jb = slot / B;
         const int id = __ldg(ids + jb);
         if (id < 0 || id > t / B) return -1;  // row() reports it
@@ -460,40 +460,52 @@ struct QQuery {
     __device__ __forceinline__ void logits(float2 (&x)[Ring::NK / 16][2][NH], const Ring& ring,
                                            uint32_t st, uint32_t live) const {
         constexpr int NG = Ring::NK / 16;
+        float acc[NG][NH][4];
+        // groups side by side, where Q's registers are not short already
+        constexpr int G = kShared ? 1 : NG;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            float acc[NH][4];
+        for (int i0 = 0; i0 < NG; i0 += G) {
+            uint32_t w[G][2][Ring::R::kKW];
 #pragma unroll
-            for (int n = 0; n < NH; ++n)
+            for (int i = 0; i < G; ++i) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-            uint32_t w0[Ring::R::kKW], w1[Ring::R::kKW];
-            ring.k_words(w0, st, 2 * i);
-            ring.k_words(w1, st, 2 * i + 1);
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i0 + i][n][e] = 0.f;
+                ring.k_words(w[i][0], st, 2 * (i0 + i));
+                ring.k_words(w[i][1], st, 2 * (i0 + i) + 1);
+            }
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t a[4];
-                k_frag<F>(w0, ks, a[0], a[2]);
-                k_frag<F>(w1, ks, a[1], a[3]);
+                uint32_t b[NH][2];
 #pragma unroll
                 for (int n = 0; n < NH; ++n) {
-                    uint32_t b[2];
                     if constexpr (kShared) {
-                        Ring::template lds<2>(b, at + (ks * NH + n) * 256);
+                        Ring::template lds<2>(b[n], at + (ks * NH + n) * 256);
                     } else {
-                        b[0] = qb[n][ks][0];
-                        b[1] = qb[n][ks][1];
+                        b[n][0] = qb[n][ks][0];
+                        b[n][1] = qb[n][ks][1];
                     }
-                    mma_f16(acc[n], a, b[0], b[1]);
+                }
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    uint32_t a[4];
+                    k_frag<F>(w[i][0], ks, a[0], a[2]);
+                    k_frag<F>(w[i][1], ks, a[1], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) mma_f16(acc[i0 + i][n], a, b[n][0], b[n][1]);
                 }
             }
+        }
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t ent = ring.entry(st, i, k, false);
                 const float2 sc = both(entry_scale(ent)), z = both(entry_zero(ent));
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
-                    x[i][k][n] = tc::ffma2(make_float2(acc[n][2 * k], acc[n][2 * k + 1]), sc,
+                    x[i][k][n] = tc::ffma2(make_float2(acc[i][n][2 * k], acc[i][n][2 * k + 1]), sc,
                                            fmul2(qsum[n], z));
             }
         }

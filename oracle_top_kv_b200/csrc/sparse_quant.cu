@@ -13,16 +13,17 @@
 namespace hs {
 namespace sq {
 
-constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kWarps = 4;      // of a decode CTA
+constexpr int kRowWarps = 1;   // of a prefill CTA: the warps work alone
+constexpr int kStages = 2;
 // 16 heads: Q in shared memory lets three CTAs share an SM without spills (2048 rows x 4
 // groups x 1024 keys: XXX us against YYY with Q in registers).
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2>;
 template <int D, int F, int NH>
-constexpr size_t kRingBytes =  // the warps' rings, then their queries
-    (size_t)kWarps * (QRing<D, F, true, kStages>::kBytes + QQuery<D, F, NH, NH == 2>::kBytes);
-// Four-warp CTAs to an SM that the registers are divided for.
-template <int NH> constexpr int kPerSm = NH == 1 ? 4 : 3;
+constexpr size_t kWarpBytes =  // a warp's ring and query
+    QRing<D, F, true, kStages>::kBytes + QQuery<D, F, NH, NH == 2>::kBytes;
+// Warps to an SM that the registers are divided for.
+template <int NH> constexpr int kPerSm = NH == 1 ? 16 : 12;
 
 // Writes a unit's heads from a warp's finished accumulators.
 template <int D, int NH, class A>
@@ -55,11 +56,11 @@ __device__ __forceinline__ void store_rows(const A& st, int g, __nv_bfloat16* o,
 }
 
 template <int D, int F, int NH>
-__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
+__global__ void __launch_bounds__(kRowWarps * 32, kPerSm<NH> / kRowWarps)
     sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                         const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
                         __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
-    const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long task = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
     if (task >= (long long)p.batch * p.hkv * p.t_q) return;
     const int j = (int)(task % p.t_q);
     const int unit = (int)(task / p.t_q);
@@ -70,10 +71,13 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     const typename A::Ring ring{smem_u32(smem_raw) + (threadIdx.x >> 5) * A::Ring::kBytes};
     A st;
     st.init(q + head0 * D, (size_t)p.t_q * D, p.group, p.scale_log2,
-            smem_u32(smem_raw) + kWarps * A::Ring::kBytes + (threadIdx.x >> 5) * decltype(st.q)::kBytes);
+            smem_u32(smem_raw) + kRowWarps * A::Ring::kBytes + (threadIdx.x >> 5) * decltype(st.q)::kBytes);
     const int n = clamp_count(cnt[task], p.ksel) * p.block_size;
     const QIndex src{idx + (size_t)task * p.ksel, n,           p.block_size,
-                     p.q_offset + j,              p.bt != nullptr, page_map(p, b, u)};
+                     p.q_offset + j,
+                     p.bt != nullptr,
+                     p.block_size % A::NK == 0 && (p.bt == nullptr || p.page_size % A::NK == 0),
+                     page_map(p, b, u)};
     st.run(ring, unit_cache<D, F>(p, cache, unit), src, 0, 1, (n + A::NK - 1) / A::NK, NoMaxima{});
     st.finish();
     store_rows<D, NH>(st, p.group, o, lse, head0, (size_t)p.t_q);
@@ -85,7 +89,7 @@ __device__ __forceinline__ float merge_weight(float m, float M) {
 }
 
 template <int D, int F, int NH>
-__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
+__global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
     decode_sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
                                const int32_t* __restrict__ seq_len,
                                const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt,
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     const typename A::Ring ring{smem_u32(smem_raw) + warp * A::Ring::kBytes};
     if (valid) {
         const int n = clamp_count(cnt[unit], p.ksel);
-        const QIndex src{idx + (size_t)unit * p.ksel, n, 1, L - 1, p.bt != nullptr,
+        const QIndex src{idx + (size_t)unit * p.ksel, n, 1, L - 1, p.bt != nullptr, false,
                          page_map(p, b, u)};
         st.run(ring, unit_cache<D, F>(p, cache, unit), src, crank * kWarps + warp, kWarps * csize,
                (n + A::NK - 1) / A::NK, NoMaxima{});
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
     st.store_part(smem + warp * kStride, g);
     __syncthreads();
     // the CTA's partial
-    float* mine = smem + kRingBytes<D, F, NH> / sizeof(float);
+    float* mine = smem + kWarps * kWarpBytes<D, F, NH> / sizeof(float);
     for (int e = threadIdx.x; e < g * D; e += blockDim.x) {
         const int h = e / D;
         float M = -INFINITY, l = 0.f, acc = 0.f;
@@ -167,10 +171,11 @@ static cudaError_t launch_sparse_t(const KParams& p, const QuantCache& c, const 
                                    cudaStream_t st) {
     const long long tasks = (long long)p.batch * p.hkv * p.t_q;
     auto kern = sparse_quant_kernel<D, F, NH>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)kRingBytes<D, F, NH>);
+    constexpr int smem = kRowWarps * (int)kWarpBytes<D, F, NH>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, kRingBytes<D, F, NH>, st>>>(
+    kern<<<(unsigned)((tasks + kRowWarps - 1) / kRowWarps), kRowWarps * 32, smem, st>>>(
         p, c, (const __nv_bfloat16*)q, idx, cnt, (__nv_bfloat16*)o, lse);
     return cudaGetLastError();
 }
@@ -180,7 +185,7 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
                                    const int32_t* seq_len, const int32_t* idx, const int32_t* cnt,
                                    void* o, float* lse, cudaStream_t st) {
     auto kern = decode_sparse_quant_kernel<D, F, NH>;
-    const size_t smem = kRingBytes<D, F, NH> + Attend<D, F, NH>::kPart * sizeof(float);
+    const size_t smem = kWarps * kWarpBytes<D, F, NH> + Attend<D, F, NH>::kPart * sizeof(float);
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
