@@ -34,25 +34,74 @@ struct Args {
 };
 constexpr int kThreads = 128;
 
+// Eight elements as they lie: 4 words of bf16 pairs, or 8 of fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load8(const T* p, uint32_t (&w)[sizeof(T) * 2]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint32_t (&w)[sizeof(T) * 2], float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+        if constexpr (sizeof(T) == 2) {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            x[i] = __uint_as_float(w[i]);
         }
-    } else {
+    }
+}
+
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Minimum and maximum of the row that LN lanes hold eight elements each of; NaN if it
+// holds one.  Both travel as one pair (minimum, - maximum).
+template <typename T, int LN>
+__device__ __forceinline__ void row_range(const uint32_t (&w)[sizeof(T) * 2], const float (&x)[8],
+                                          float& lo, float& hi) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t a = min_nan2(min_nan2(w[0], w[1]), min_nan2(w[2], w[3]));
+        const uint32_t b = max_nan2(max_nan2(w[0], w[1]), max_nan2(w[2], w[3])) ^ 0x80008000u;
+        uint32_t m = min_nan2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-            x[4 * i] = v.x;
-            x[4 * i + 1] = v.y;
-            x[4 * i + 2] = v.z;
-            x[4 * i + 3] = v.w;
+        for (int s = 1; s < LN; s <<= 1) m = min_nan2(m, __shfl_xor_sync(0xffffffffu, m, s));
+        lo = __uint_as_float(m << 16);
+        hi = -__uint_as_float(m & 0xffff0000u);
+    } else {
+        lo = x[0];
+        hi = -x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            lo = min_nan(lo, x[i]);
+            hi = min_nan(hi, -x[i]);
         }
+#pragma unroll
+        for (int s = 1; s < LN; s <<= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+            hi = min_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+        }
+        hi = -hi;
     }
 }
 
@@ -121,20 +170,28 @@ __device__ __forceinline__ void encode8_exact(const float (&x)[8], float s, floa
 }
 // The same codes with y = (x - z) r, r = 1 / s to 2^-22, in place of the quotient: false if a
 // quotient may lie on the other side of a border between two codes than y does.
-template <int F>
+template <int F, bool kClamp>
 __device__ __forceinline__ bool encode8_near(const float (&x)[8], float r, float z, uint32_t (&w)[2]) {
     w[0] = w[1] = 0u;
     if constexpr (F == HS_KV_INT4) {
         constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer
-        float far = 0.f;
+        float far = 0.f, d[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float y = fminf(fmaxf((x[i] - z) * r, 0.f), 15.f);
+        for (int i = 7; i >= 0; --i) {
+            float y = (x[i] - z) * r;
+            // bf16 rows: zero is their minimum itself, and 15 scale at least their range
+            // less 2^-9 of it, so 0 <= y < 15.1
+            if constexpr (kClamp) y = fminf(fmaxf(y, 0.f), 15.f);
             const float c = y + kMagic;
-            far = fmaxf(far, fabsf(y - (c - kMagic)));
-            w[0] |= (__float_as_uint(c) & 15u) << (4 * i);
+            d[i] = fabsf(y - (c - kMagic));
+            w[0] = w[0] * 16u + __float_as_uint(c);
         }
-        return far < 0.49998f;  // y <= 15 is off by less than 1e-5
+        // what the magic number's bits added up to
+        constexpr uint32_t kBits = 0x4b400000u;
+        w[0] -= kBits * 0x11111111u;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) far = tc::max3f(far, d[i], d[i + 1]);
+        return far < 0.49998f;  // y is off by less than 1e-5
     } else {
         uint32_t v[2] = {0u, 0u};
 #pragma unroll
@@ -156,34 +213,24 @@ __global__ void __launch_bounds__(kThreads) kv_quant_write_kernel(Args a) {
     const Rows rows(a, PASS * kRows);
     const int c = threadIdx.x % LN, side = blockIdx.y;
     const T* src = (const T*)a.x[side];
-    float x[kRows][8];
+    uint32_t raw[kRows][sizeof(T) * 2];
     const int j0 = rows.j0 + threadIdx.x / LN;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         const int j = j0 + k * PASS;
         if (j < rows.n) {
-            load8(src + rows.at(a.p, j) * D + c * 8, x[k]);
+            load8(src + rows.at(a.p, j) * D + c * 8, raw[k]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
+            for (int i = 0; i < (int)sizeof(T) * 2; ++i) raw[k][i] = 0u;
         }
     }
-    const uint32_t seg = ((1u << (LN & 31)) - 1u) << ((threadIdx.x & 31) / LN * LN);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
-        float lo = x[k][0], hi = x[k][0], sum = 0.f;  // sum: a NaN or an infinity shows in it
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, x[k][i]);
-            hi = fmaxf(hi, x[k][i]);
-            sum = fmaf(x[k][i], 0.f, sum);
-        }
-#pragma unroll
-        for (int m = 1; m < LN; m <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-        }
-        const bool bad = (__ballot_sync(0xffffffffu, sum != 0.f) & seg) != 0u;
+        float x[8];
+        unpack8<T>(raw[k], x);
+        float lo, hi;
+        row_range<T, LN>(raw[k], x, lo, hi);
         float s, z;
         if constexpr (F == HS_KV_INT4) {
             s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)));
@@ -192,13 +239,13 @@ __global__ void __launch_bounds__(kThreads) kv_quant_write_kernel(Args a) {
             s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(fmaxf(fabsf(lo), fabsf(hi)), 448.f)));
             z = 0.f;
         }
-        if (bad || !isfinite(s) || !isfinite(z)) s = z = __int_as_float(0x7fc00000);
+        if (!isfinite(s) || !isfinite(z) || lo != lo) s = z = __int_as_float(0x7fc00000);
         const long long row = rows.row(a.p, j0 + k * PASS);
         if (row < 0) continue;
         uint32_t w[2];
         // a reciprocal that is a normal number, and quotients that fit
-        if (!(s > 1e-30f && s < 1e30f) || !encode8_near<F>(x[k], __frcp_rn(s), z, w))
-            encode8_exact<F>(x[k], s, z, w);
+        if (!(s > 1e-30f && s < 1e30f) || !encode8_near<F, sizeof(T) != 2>(x, __frcp_rn(s), z, w))
+            encode8_exact<F>(x, s, z, w);
         if constexpr (F == HS_KV_INT4)
             *reinterpret_cast<uint32_t*>(a.codes[side] + row * (D / 2) + c * 4) = w[0];
         else

@@ -172,9 +172,7 @@ static cudaError_t launch_sparse_t(const KParams& p, const QuantCache& c, const 
     const long long tasks = (long long)p.batch * p.hkv * p.t_q;
     auto kern = sparse_quant_kernel<D, F, NH>;
     constexpr int smem = kRowWarps * (int)kWarpBytes<D, F, NH>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static_assert(smem <= 48 * 1024, "more needs the kernel's attribute set");
     kern<<<(unsigned)((tasks + kRowWarps - 1) / kRowWarps), kRowWarps * 32, smem, st>>>(
         p, c, (const __nv_bfloat16*)q, idx, cnt, (__nv_bfloat16*)o, lse);
     return cudaGetLastError();

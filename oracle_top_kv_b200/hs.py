@@ -124,13 +124,20 @@ def load(path: str = LIB_PATH):
     return lib
 
 
+# The calls behind torch.cuda.current_device() and current_stream(), without the objects
+# that those make (a microsecond or more per call of this module).
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise ValueError("expected a CUDA tensor")
+    if device != _current_device():
+        raise ValueError("expected a tensor on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
@@ -138,7 +145,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
