@@ -88,6 +88,18 @@ __device__ __forceinline__ float merge_weight(float m, float M) {
     return m == -INFINITY ? 0.f : exp2f(m - M);
 }
 
+// Four fp32 at shared address `a` of cluster CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a, uint32_t rank) {
+    uint32_t ra;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(ra)
+                 : "memory");
+    return v;
+}
+
 template <int D, int F, int NH>
 __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
     decode_sparse_quant_kernel(KParams p, QuantCache cache, const __nv_bfloat16* __restrict__ q,
@@ -124,43 +136,69 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
     st.finish();
     st.store_part(smem + warp * kStride, g);
     __syncthreads();
-    // the CTA's partial
+    // the CTA's partial: weights of the warps' first, then the sums
     float* mine = smem + kWarps * kWarpBytes<D, F, NH> / sizeof(float);
-    for (int e = threadIdx.x; e < g * D; e += blockDim.x) {
-        const int h = e / D;
-        float M = -INFINITY, l = 0.f, acc = 0.f;
+    __shared__ float s_f[8][16], s_scale[16];  // weights per (warp, then CTA) and head
+    const int h16 = threadIdx.x & 15, w16 = threadIdx.x >> 4;
+    if (w16 < kWarps && h16 < g) {
+        float m[kWarps], M = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, smem[w * kStride + 2 * h]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m[w] = smem[w * kStride + 2 * h16]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += smem[w * kStride + 2 * h16 + 1] * merge_weight(m[w], M);
+        s_f[w16][h16] = merge_weight(smem[w16 * kStride + 2 * h16], M);
+        if (w16 == 0) {
+            mine[2 * h16] = M;
+            mine[2 * h16 + 1] = l;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < g * (D / 4); e += blockDim.x) {
+        const int h = e / (D / 4);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = merge_weight(smem[w * kStride + 2 * h], M);
-            l += smem[w * kStride + 2 * h + 1] * f;
-            acc += smem[w * kStride + 32 + e] * f;
+            const float f = s_f[w][h];
+            const float4 x = reinterpret_cast<const float4*>(smem + w * kStride + 32)[e];
+            a.x += x.x * f;
+            a.y += x.y * f;
+            a.z += x.z * f;
+            a.w += x.w * f;
         }
-        mine[32 + e] = acc;
-        if (e % D == 0) {
-            mine[2 * h] = M;
-            mine[2 * h + 1] = l;
-        }
+        reinterpret_cast<float4*>(mine + 32)[e] = a;
     }
     if (csize > 1) cluster_sync_all();
     else __syncthreads();
-    // each CTA of the cluster writes a share of the heads
+    // the cluster's: weights again, then each CTA writes a share of the outputs
     const uint32_t at = smem_u32(mine);
-    auto rd = [&](int r, int off) -> float {
-        return csize > 1 ? ld_cluster_f32(at + 4u * off, (uint32_t)r) : mine[off];
-    };
-    for (int e = crank * blockDim.x + threadIdx.x; e < g * D; e += csize * blockDim.x) {
-        const int h = e / D;
-        float M = -INFINITY, l = 0.f, acc = 0.f;
-        for (int r = 0; r < csize; ++r) M = fmaxf(M, rd(r, 2 * h));
-        for (int r = 0; r < csize; ++r) {
-            const float f = merge_weight(rd(r, 2 * h), M);
-            l += rd(r, 2 * h + 1) * f;
-            acc += rd(r, 32 + e) * f;
+    if (w16 < csize && h16 < g) {
+        float M = -INFINITY, l = 0.f;
+        for (int r = 0; r < csize; ++r) M = fmaxf(M, ld_cluster_f32(at + 8u * h16, (uint32_t)r));
+        for (int r = 0; r < csize; ++r)
+            l += ld_cluster_f32(at + 8u * h16 + 4u, (uint32_t)r) *
+                 merge_weight(ld_cluster_f32(at + 8u * h16, (uint32_t)r), M);
+        s_f[w16][h16] = merge_weight(ld_cluster_f32(at + 8u * h16, (uint32_t)w16), M);
+        if (w16 == 0) {
+            s_scale[h16] = l == 0.f ? 0.f : 1.f / l;
+            if (crank == 0 && lse) lse[head0 + h16] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
         }
-        o[(head0 + h) * D + e % D] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
-        if (e % D == 0 && lse) lse[head0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+    __syncthreads();
+    for (int e = crank * blockDim.x + threadIdx.x; e < g * (D / 4); e += csize * blockDim.x) {
+        const int h = e / (D / 4);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < csize; ++r) {
+            const float f = s_f[r][h];
+            const float4 x = ld_cluster_f32x4(at + 128u + 16u * e, (uint32_t)r);
+            a.x += x.x * f;
+            a.y += x.y * f;
+            a.z += x.z * f;
+            a.w += x.w * f;
+        }
+        const float inv = s_scale[h];
+        *reinterpret_cast<uint2*>(o + head0 * D + 4 * e) =
+            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     }
     if (csize > 1) cluster_sync_all();  // peers keep their shared memory until all have read
 }
