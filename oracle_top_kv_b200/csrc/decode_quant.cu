@@ -6,18 +6,19 @@
 //     KV group) units, laid end to end, are cut into equal shares, one per CTA
 //     of a grid that fills the GPU once: ragged batches and few long sequences
 //     keep every SM busy alike.  A CTA writes one partial (m, l, O) per unit
-//     that its share touches, and every step's largest logit per head.
+//     that its share touches, and every 16 keys' largest logit per head.
 //  2. decode_quant_select_kernel, a cluster per unit: the exact log-sum-exp
 //     merge -> o, lse, then the index set.  The group score max_h (a2_h -
 //     lse2_h) of a key needs every head's final lse, so it cannot be ranked in
 //     pass 1.  Instead of carrying every logit over (64 bytes a key, against rows
-//     of 68 or 132), the maxima bound it: a tile of one step's keys has the
-//     largest score max_h (max_i a2_hi - lse2_h), exactly.  Each of the k - w best
-//     tiles (equal bounds: lower tile first) holds a key at least as good as
-//     every key of the others, so the k - w best keys lie in those tiles, and
-//     none is below the last one's bound.  Only they are read again (at most
-//     32 (k - w) keys), and of their keys only those that reach that bound are
-//     ranked.
+//     of 68 or 132), the maxima bound it: a tile of 16 keys has the largest score
+//     max_h (max_i a2_hi - lse2_h), exactly.  Each of the k - w best tiles (equal
+//     bounds: lower tile first) holds a key at least as good as every key of the
+//     others, so the k - w best keys lie in those tiles, and none is below the
+//     last one's bound.  Only they are read again (at most 16 (k - w + kSlack)
+//     keys), and of their keys only those that reach that bound are ranked.
+//     Tiles of 32 keys: 13 us less in pass 1 (their maxima are fewer), 37 us more
+//     here (32 sequences of 131072 keys, 4-bit, 16 heads: 567 + 144 us against 580 + 107).
 #include <atomic>
 
 #include "cta_select.cuh"
@@ -38,7 +39,13 @@ template <int NH> constexpr int kPerSm = NH == 1 ? 4 : 2;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBoundCap = 16384;  // tile bounds a selecting CTA holds on chip
-template <int D, int F> using SelRing = QRing<D, F, false, 3>;
+constexpr int kSub = 16;  // keys of a tile of the selection
+// Tiles that may be rescored past the k - w best: the threshold is then found in fewer
+// passes (one sequence of 2^20 keys 64.9 -> 62.6 us; at 64 the further tiles cost more
+// than the passes, 8-bit ragged batch 52.6 -> 58.4 us).
+constexpr int kSlack = 16;
+// Ring of a rescoring warp (some 100 KB for the CTA's 16).
+template <int D, int F> using KeyRing = QRing<D, F, false, 3>;
 // Rounds of rescoring between looks at the number of candidates, where the buffer for
 // that many fits (budgets k - w up to about 3000); else 1.
 constexpr int kCheck = 4;
@@ -101,31 +108,41 @@ __device__ __forceinline__ int share_of(long long x, int G, long long total) {
     return (int)(((x + 1) * G - 1) / total);
 }
 
-// Reduces each step's maxima over the keys and stores them: each halving of the
-// lanes of equal t drops half of the lane's heads.
+// Reduces the maxima of a step's 16-key groups over the keys and stores them: a lane has
+// V of them (group, head), and each halving of the lanes of equal t drops half of those.
 struct TileMaxima {
     float* at;  // this unit's [tiles][16]
-    template <int NH>
-    __device__ __forceinline__ void operator()(int step, const float2 (&m)[NH]) const {
+    template <int NG, int NH>
+    __device__ __forceinline__ void operator()(int step, const float2 (&m)[NG][NH]) const {
+        constexpr int V = 2 * NG * NH;
         const int lane = threadIdx.x & 31;
-        auto halve = [&](float a, float b, int bit) {  // a where the bit is clear
-            const float got = __shfl_xor_sync(0xffffffffu, lane & bit ? a : b, bit);
-            return fmaxf(lane & bit ? b : a, got);
-        };
-        float v;
-        int h = 2 * (lane & 3);
-        if constexpr (NH == 2) {
-            const float x = halve(m[0].x, m[1].x, 16), y = halve(m[0].y, m[1].y, 16);
-            v = halve(x, y, 8);
-            h += (lane & 16 ? 8 : 0) + (lane & 8 ? 1 : 0);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        } else {
-            v = halve(m[0].x, m[0].y, 16);
-            h += lane & 16 ? 1 : 0;
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                v[2 * (i * NH + n)] = m[i][n].x;
+                v[2 * (i * NH + n) + 1] = m[i][n].y;
+            }
+        int which = 0, left = V;
+#pragma unroll
+        for (int bit = 16; bit >= 4; bit >>= 1) {
+            left >>= 1;
+            if (left > 0) {
+                which = 2 * which + (lane & bit ? 1 : 0);
+#pragma unroll
+                for (int c = 0; c < left; ++c) {
+                    const float give = lane & bit ? v[c] : v[c + left];
+                    const float keep = lane & bit ? v[c + left] : v[c];
+                    v[c] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+                }
+            } else {
+                v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+            }
         }
-        if (!(lane & (NH == 2 ? 4 : 12))) at[(size_t)step * 16 + h] = v;
+        const int h = 8 * ((which >> 1) % NH) + 2 * (lane & 3) + (which & 1);
+        if (V == 8 || !(lane & (V == 4 ? 4 : 12)))
+            at[(size_t)step * (16 * NG) + 16 * ((which >> 1) / NH) + h] = v[0];
     }
 };
 
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
         const QuantCache uc = unit_cache<D, F>(p, cache, unit);
         const int L = __ldg(seq_len + b);
         const TileMaxima tm{ws.tmax + (size_t)unit * ws.tiles * 16};
-        if (p.bt) st.run(ring, uc, QPagedRange{L, page_map(p, b, u)}, s0 + warp, kWarps, s1, tm);
+        if (p.bt) st.run(ring, uc, QRange<NK>{L, page_map(p, b, u)}, s0 + warp, kWarps, s1, tm);
         else st.template run_dense<kWarps>(ring, uc, L, s0 + warp, s1, tm);
         st.finish();
         st.store_part(smem + warp * kStride, g);
@@ -226,13 +243,25 @@ __device__ __forceinline__ T* cluster_ptr(T* a, int rank) {
     return r;
 }
 
-// cta_kth_largest over the keys of all C CTAs of the cluster: get(0) ..
-// get(n - 1) are this CTA's.  All threads of all CTAs call; all get the result.
+// A key t such that at least k and at most k + kSlack of the distinct keys of all C CTAs
+// of the cluster are >= t (fewer than k + 1 keys: the least): get(0) .. get(n - 1) are
+// this CTA's.  All threads of all CTAs call; all get the result.  Range bucket select as
+// cta_kth_largest, which ends as soon as the bucket that holds the k-th largest fits
+// into the slack; each CTA counts, CTA 0 sums.
+struct ThresholdSmem {
+    uint32_t hist[2][256];
+    unsigned long long lo, hi;
+    unsigned long long nlo, nhi;
+    int need, done;
+};
 template <typename Get>
-__device__ uint64_t cluster_kth_largest(Get get, int n, int k, CtaSelectSmem& sh, int C, int rank) {
-    if (C == 1) return cta_kth_largest(get, n, k, sh);
+__device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, int C, int rank) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-    CtaSelectSmem* root = cluster_ptr(&sh, 0);
+    ThresholdSmem* root = C > 1 ? cluster_ptr(&sh, 0) : &sh;
+    auto sync = [&] {
+        if (C > 1) cluster_sync_all();
+        else __syncthreads();
+    };
     uint64_t mn = ~0ull, mx = 0ull;
     for (int i = tid; i < n; i += nt) {
         const uint64_t v = get(i);
@@ -245,36 +274,35 @@ __device__ uint64_t cluster_kth_largest(Get get, int n, int k, CtaSelectSmem& sh
         mn = a < mn ? a : mn;
         mx = b > mx ? b : mx;
     }
-    if (tid == 0) { sh.lo = ~0ull; sh.hi = 0ull; sh.found = 0ull; }
-    cluster_sync_all();
+    if (tid == 0) { sh.lo = ~0ull; sh.hi = 0ull; }
+    for (int x = tid; x < 512; x += nt) (&sh.hist[0][0])[x] = 0u;
+    sync();
     if (lane == 0 && mn <= mx) {
         atomicMin(&root->lo, (unsigned long long)mn);
         atomicMax(&root->hi, (unsigned long long)mx);
     }
-    cluster_sync_all();
+    sync();
     uint64_t lo = *(volatile unsigned long long*)&root->lo;
     uint64_t hi = *(volatile unsigned long long*)&root->hi;
     int need = k;
-    __shared__ uint64_t s_lo, s_hi;
-    __shared__ int s_need, s_single;
-    for (int pass = 0; pass < 9 && lo != hi; ++pass) {
-        const int shift = max(0, top_bit64(hi - lo) - 7);
-        for (int x = tid; x < 256; x += nt) sh.hist[x] = 0u;
-        __syncthreads();
+    for (int pass = 0; pass < 9 && lo < hi; ++pass) {
+        const int h = pass & 1, shift = max(0, top_bit64(hi - lo) - 7);
         for (int i = tid; i < n; i += nt) {
             const uint64_t v = get(i);
-            if (v >= lo && v <= hi) atomicAdd(&sh.hist[(uint32_t)((v - lo) >> shift)], 1u);
+            if (v >= lo && v <= hi) atomicAdd(&sh.hist[h][(uint32_t)((v - lo) >> shift)], 1u);
         }
-        cluster_sync_all();  // the root's histogram is zeroed and counted
-        if (rank != 0)
-            for (int x = tid; x < 256; x += nt)
-                if (sh.hist[x]) atomicAdd(&root->hist[x], sh.hist[x]);
-        cluster_sync_all();
+        sync();
+        if (C > 1) {
+            if (rank != 0)
+                for (int x = tid; x < 256; x += nt)
+                    if (sh.hist[h][x]) atomicAdd(&root->hist[h][x], sh.hist[h][x]);
+            cluster_sync_all();
+        }
         if (tid < 32) {
             uint32_t c[8], s = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                c[j] = *(volatile uint32_t*)&root->hist[255 - 8 * lane - j];
+                c[j] = *(volatile uint32_t*)&root->hist[h][255 - 8 * lane - j];
                 s += c[j];
             }
             uint32_t incl = s;  // lane l owns buckets 255 - 8l .. 248 - 8l, from the top
@@ -290,92 +318,91 @@ __device__ uint64_t cluster_kth_largest(Get get, int n, int k, CtaSelectSmem& sh
                 while (above + c[j] < (uint32_t)need) { above += c[j]; ++j; }
                 const uint64_t nlo = lo + ((uint64_t)(255u - 8u * lane - j) << shift);
                 const uint64_t span = (1ull << shift) - 1ull;
-                s_lo = nlo;
-                s_hi = hi - nlo < span ? hi : nlo + span;
-                s_need = need - (int)above;
-                s_single = c[j] == 1u;
+                sh.nlo = nlo;
+                sh.nhi = hi - nlo < span ? hi : nlo + span;
+                sh.need = need - (int)above;
+                sh.done = (int)(above + c[j]) <= need + kSlack;
             }
         }
+        // the other histogram was last read before the sync above
+        for (int x = tid; x < 256; x += nt) sh.hist[h ^ 1][x] = 0u;
         __syncthreads();
-        lo = s_lo;
-        hi = s_hi;
-        need = s_need;
-        const bool single = s_single != 0;
-        if (single && lo != hi) {  // the bucket holds one key: its CTA tells the others
-            for (int i = tid; i < n; i += nt) {
-                const uint64_t v = get(i);
-                if (v >= lo && v <= hi)
-                    for (int r = 0; r < C; ++r)
-                        *(volatile unsigned long long*)&cluster_ptr(&sh, r)->found = v;
-            }
-            cluster_sync_all();
-            return sh.found;
-        }
-        cluster_sync_all();  // every CTA has read the root's histogram
+        lo = sh.nlo;
+        hi = sh.nhi;
+        need = sh.need;
+        const bool done = sh.done != 0;
+        __syncthreads();  // read by all before the next pass writes
+        if (done) break;
     }
+    if (C > 1) cluster_sync_all();  // CTA 0 keeps its histograms until all have read them
     return lo;
 }
 
-// Rows of listed tiles of NK keys (slot = place in the list * NK + key of the
-// tile), keys below `end` only.
+// Keys of `n` listed tiles, NK / kSub of them a step, below `end` only.
 template <int NK>
 struct QTiles {
     const int* tiles;
-    int n_tiles, end;
-    bool paged;
+    int n, end;
     PageMap pm;
-    __device__ __forceinline__ int key(int slot) const { return tiles[slot / NK] * NK + slot % NK; }
-    __device__ __forceinline__ int row(int slot) const {
-        const int k = key(slot);
-        return k >= end ? -1 : paged ? pm.row(k) : k;
+    static constexpr int kPer = NK / kSub;
+    __device__ __forceinline__ int steps() const { return (n + kPer - 1) / kPer; }
+    __device__ __forceinline__ bool runs() const { return kPer == 1; }
+    __device__ __forceinline__ int limit() const { return end; }
+    __device__ __forceinline__ int load(int step) const {
+        const int i = step * kPer + (int)(threadIdx.x & (NK - 1)) / kSub;
+        return i < n ? tiles[i] : -1;
     }
-    __device__ __forceinline__ int run(int slot, int N) const {
-        const int k = key(slot);
-        if (k + N > end || (paged && pm.page_size % N)) return -1;
-        return paged ? pm.row(k) : k;
+    __device__ __forceinline__ int key(int tile, int) const {
+        if (tile < 0) return -1;
+        const int k = tile * kSub + (kPer == 1 ? 0 : (int)(threadIdx.x & (kSub - 1)));
+        return k < end ? k : -1;
+    }
+    __device__ __forceinline__ int key_at(int step, int x) const {
+        return tiles[step * kPer + x / kSub] * kSub + x % kSub;
     }
 };
-// Consecutive keys first .. end - 1.
+// Keys first .. end - 1, every C-th run of NK of them from the rank-th on.
+template <int NK>
 struct QKeys {
-    int first, end;
-    bool paged;
+    int first, end, C, rank;
     PageMap pm;
-    __device__ __forceinline__ int key(int slot) const { return first + slot; }
-    __device__ __forceinline__ int row(int slot) const {
-        const int k = first + slot;
-        return k >= end ? -1 : paged ? pm.row(k) : k;
+    __device__ __forceinline__ int steps() const {
+        const int all = (end - first + NK - 1) / NK;
+        return all > rank ? (all - rank - 1) / C + 1 : 0;
     }
-    __device__ __forceinline__ int run(int, int) const { return -1; }
+    __device__ __forceinline__ bool runs() const { return true; }
+    __device__ __forceinline__ int limit() const { return end; }
+    __device__ __forceinline__ int load(int) const { return 0; }
+    __device__ __forceinline__ int key(int, int step) const { return first + (step * C + rank) * NK; }
+    __device__ __forceinline__ int key_at(int step, int x) const { return key(0, step) + x; }
 };
 
 // Rescores a source's keys, warp w of the CTA steps w, w + kSelWarps, ...: put(key,
 // score, log2 domain) for each; after_rounds() by all threads, once per `check` rounds.
-template <int D, int F, int NH, class Src, class Put, class After>
+template <class Ring, int D, int F, int NH, class Src, class Put, class After>
 __device__ __forceinline__ void score_keys(const QQuery<D, F, NH>& q, const float2 (&lse2)[NH],
                                            uint32_t ring_base, const QuantCache& c, const Src& src,
                                            int n_steps, int check, Put put, After after_rounds) {
-    using Ring = SelRing<D, F>;
     constexpr int NK = Ring::NK;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
     const Ring ring{ring_base + warp * Ring::kBytes};
     int ahead = warp;
-    QPlace at = place_of<NK>(src, ahead, n_steps);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (ahead < n_steps) ring.fill(i, c, at);
+    QPlace at = find<NK>(src, warp < n_steps ? src.load(warp) : 0, warp, n_steps);
+    constexpr int S = Ring::kDepth;
+    auto fill = [&](int s) {
+        if (ahead < n_steps) ring.fill(s, c, row_of(src.pm, at), at.run);
         cp_async_commit();
         ahead += kSelWarps;
-        at = place_of<NK>(src, ahead, n_steps);
-    }
+        at = find<NK>(src, ahead < n_steps ? src.load(ahead) : 0, ahead, n_steps);
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fill(i);
     int s = 0, rounds = 0;
     for (int r0 = 0; r0 < n_steps; r0 += kSelWarps) {
         const int st = r0 + warp;
-        cp_async_wait<1>();
+        cp_async_wait<S - 2>();
         __syncwarp();
-        if (ahead < n_steps) ring.fill(s == 0 ? 2 : s - 1, c, at);
-        cp_async_commit();
-        ahead += kSelWarps;
-        at = place_of<NK>(src, ahead, n_steps);
+        fill(s == 0 ? S - 1 : s - 1);
         if (st < n_steps) {
             const uint32_t live = ring.live(s);
             float2 x[NK / 16][2][NH];
@@ -393,10 +420,10 @@ __device__ __forceinline__ void score_keys(const QQuery<D, F, NH>& q, const floa
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                     const int slot = 16 * i + 8 * k + (gid >> 1) + 4 * (gid & 1);
-                    if (t == 0 && ((live >> slot) & 1u)) put(src.key(st * NK + slot), v);
+                    if (t == 0 && ((live >> slot) & 1u)) put(src.key_at(st, slot), v);
                 }
         }
-        s = s == 2 ? 0 : s + 1;
+        s = s == S - 1 ? 0 : s + 1;
         if (++rounds == check) {
             rounds = 0;
             after_rounds();
@@ -468,15 +495,14 @@ __device__ void sort_ascending(uint64_t* a, int n) {
 // Dynamic shared memory of the selection, for Kc = k - w.
 template <int D, int F>
 struct SelSmem {
+    static constexpr size_t most(size_t a, size_t b) { return a > b ? a : b; }
     static constexpr size_t kFront =  // rings; before that, tile bounds or the merge's sums
-        (size_t)kSelWarps * SelRing<D, F>::kBytes > sizeof(uint32_t) * kBoundCap
-            ? (size_t)kSelWarps * SelRing<D, F>::kBytes
-            : sizeof(uint32_t) * kBoundCap;
-    static constexpr int kRound = kSelWarps * SelRing<D, F>::NK;  // keys of a round
+        most(kSelWarps * (size_t)KeyRing<D, F>::kBytes, sizeof(uint32_t) * kBoundCap);
+    static constexpr int kRound = kSelWarps * KeyRing<D, F>::NK;  // keys of a round, at most
     __host__ __device__ static int cap(int Kc, int check) { return 2 * Kc + check * kRound; }
     __host__ __device__ static int sort_n(int Kc) { return next_pow2(Kc > 0 ? Kc : 1); }
     __host__ __device__ static size_t bytes(int Kc, int check) {
-        return kFront + sizeof(uint64_t) * (cap(Kc, check) + sort_n(Kc)) + sizeof(int) * (Kc + 2);
+        return kFront + sizeof(uint64_t) * (cap(Kc, check) + sort_n(Kc)) + sizeof(int) * (Kc + 2 + kSlack);
     }
     static constexpr size_t kMost = 232448 - 4096;  // a CTA's shared memory, less the static part
     static int check(int Kc) { return bytes(Kc, kCheck) <= kMost ? kCheck : 1; }
@@ -491,9 +517,9 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                                float* __restrict__ sel) {
     using A = Attend<D, F, NH>;
     using S = SelSmem<D, F>;
-    constexpr int NK = A::NK;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ CtaSelectSmem cs;
+    __shared__ ThresholdSmem ts;
     __shared__ float s_m[16], s_lse2[16];
     __shared__ int s_n, s_list, s_cut;
     __shared__ unsigned long long s_thr;
@@ -504,7 +530,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     const size_t head0 = (size_t)b * p.hq + (size_t)u * g;
     int32_t* irow = idx + (size_t)unit * p.ksel;
     float* srow = sel ? sel + (size_t)unit * p.ksel : nullptr;
-    const int n = seq_steps<NK>(seq_len, b, p.t_kv);
+    const int n = seq_steps<A::NK>(seq_len, b, p.t_kv);
     if (n == 0) {  // length out of range: nothing attended, nothing selected
         if (rank != 0) return;
         for (int x = tid; x < g * D; x += blockDim.x) o[head0 * D + x] = __float2bfloat16_rn(0.f);
@@ -520,8 +546,8 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     if (tid < 16) s_lse2[tid] = INFINITY;  // heads past the group never score
     __syncthreads();
     {
-        const long long before = sum_steps<NK>(seq_len, 0, b, p.t_kv);
-        const long long total = (before + sum_steps<NK>(seq_len, b, p.batch, p.t_kv)) * p.hkv;
+        const long long before = sum_steps<A::NK>(seq_len, 0, b, p.t_kv);
+        const long long total = (before + sum_steps<A::NK>(seq_len, b, p.batch, p.t_kv)) * p.hkv;
         const long long first = before * p.hkv + (long long)u * n;
         const int G = ctas_used(grid1, total);
         const int c0 = share_of(first, G, total), parts = share_of(first + n - 1, G, total) - c0 + 1;
@@ -590,10 +616,9 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     if (!ranked && rank != 0) return;
     const QuantCache uc = unit_cache<D, F>(p, cache, unit);
     const PageMap pm = page_map(p, b, u);
-    const bool paged = p.bt != nullptr;
     uint64_t* buf = reinterpret_cast<uint64_t*>(smem_raw + S::kFront);  // [cap(Kc)]
     uint64_t* tmp = buf + S::cap(Kc, check);                                    // [sort_n(Kc)]
-    int* list = reinterpret_cast<int*>(tmp + S::sort_n(Kc));             // [Kc + 2]
+    int* list = reinterpret_cast<int*>(tmp + S::sort_n(Kc));             // [Kc + 2 + kSlack]
     QQuery<D, F, NH> qq;
     float2 nl[NH];
     if (ranked || srow) {
@@ -608,14 +633,31 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     __syncthreads();
     int n_best = 0;
     if (ranked) {
-        const int full = lo / NK;  // tiles of ranked keys only; tile `full` has some if lo % NK
+        const int full = lo / kSub;  // tiles of ranked keys only; tile `full` has some if lo % kSub
         // this CTA's tiles: chunks of 32, dealt out over the cluster
         const int chunks = (full + 31) / 32;
         const int mine = (chunks > rank ? (chunks - rank - 1) / C + 1 : 0) * 32;
         auto tile = [&](int i) { return ((i >> 5) * C + rank) * 32 + (i & 31); };
-        if (full <= Kc) {
-            for (int i = tid; i < mine; i += blockDim.x)
-                if (tile(i) < full) list[atomicAdd(&s_list, 1)] = tile(i);
+        auto offer = [&](int key, float v) {
+            const uint64_t c = sel_key(v, (uint32_t)key);
+            if (c >= s_thr) buf[atomicAdd(&s_n, 1)] = c;
+        };
+        const int cap = S::cap(Kc, check);
+        auto look = [&] {
+            __syncthreads();
+            const int have = s_n;
+            __syncthreads();  // read by all before the next offers
+            if (have > cap - check * S::kRound) {
+                uint64_t kth;
+                keep_largest(buf, have, Kc, tmp, cs, &s_cut, &kth);
+                if (tid == 0) { s_thr = kth; s_n = Kc; }
+                __syncthreads();
+            }
+        };
+        if (full <= Kc) {  // no tile can be left out
+            using Ring = KeyRing<D, F>;
+            const QKeys<Ring::NK> src{0, lo, C, rank, pm};
+            score_keys<Ring, D, F, NH>(qq, nl, smem_u32(smem_raw), uc, src, src.steps(), check, offer, look);
         } else {
             const float4* tm = reinterpret_cast<const float4*>(ws.tmax + (size_t)unit * ws.tiles * 16);
             uint32_t* bits = mine <= kBoundCap ? reinterpret_cast<uint32_t*>(smem_raw)
@@ -652,7 +694,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
             auto key = [&](int i) -> uint64_t {
                 return ((uint64_t)bits[i] << 32) | (uint64_t)(0xffffffffu - (uint32_t)tile(i));
             };
-            const uint64_t kth = cluster_kth_largest(key, mine, Kc, cs, C, rank);
+            const uint64_t kth = cluster_threshold(key, mine, Kc, ts, C, rank);
             for (int i = tid; i < mine; i += blockDim.x)
                 if (key(i) >= kth) list[atomicAdd(&s_list, 1)] = tile(i);
             if (tid == 0) {
@@ -663,29 +705,13 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                 for (int h = 0; h < g; ++h) mag = fmaxf(mag, fabsf(s_lse2[h]));
                 s_thr = isfinite(mag) ? (uint64_t)float_order(th - 4e-6f * mag) << 32 : 0ull;
             }
+            __syncthreads();
+            if (tid == 0 && rank == 0 && lo % kSub != 0) list[s_list++] = full;
+            __syncthreads();
+            using Ring = KeyRing<D, F>;
+            const QTiles<Ring::NK> src{list, s_list, lo, pm};
+            score_keys<Ring, D, F, NH>(qq, nl, smem_u32(smem_raw), uc, src, src.steps(), check, offer, look);
         }
-        __syncthreads();
-        if (tid == 0 && rank == 0 && lo % NK != 0) list[s_list++] = full;
-        __syncthreads();
-        const QTiles<NK> src{list, s_list, lo, paged, pm};
-        const int cap = S::cap(Kc, check);
-        score_keys<D, F, NH>(
-            qq, nl, smem_u32(smem_raw), uc, src, s_list, check,
-            [&](int key, float v) {
-                const uint64_t c = sel_key(v, (uint32_t)key);
-                if (c >= s_thr) buf[atomicAdd(&s_n, 1)] = c;
-            },
-            [&] {
-                __syncthreads();
-                const int have = s_n;
-                __syncthreads();  // read by all before the next offers
-                if (have > cap - check * S::kRound) {
-                    uint64_t kth;
-                    keep_largest(buf, have, Kc, tmp, cs, &s_cut, &kth);
-                    if (tid == 0) { s_thr = kth; s_n = Kc; }
-                    __syncthreads();
-                }
-            });
         __syncthreads();
         n_best = s_n;
         uint64_t kth;
@@ -730,8 +756,10 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     if (tid == 0) cnt[unit] = n_out;
     if (srow) {
         __syncthreads();
-        score_keys<D, F, NH>(
-            qq, nl, smem_u32(smem_raw), uc, QKeys{lo, L, paged, pm}, (L - lo + NK - 1) / NK, 1,
+        using Ring = KeyRing<D, F>;
+        const QKeys<Ring::NK> src{lo, L, 1, 0, pm};
+        score_keys<Ring, D, F, NH>(
+            qq, nl, smem_u32(smem_raw), uc, src, src.steps(), 1,
             [&](int key, float v) { srow[n_best + key - lo] = exp2f(v); }, [] {});
     }
 }

@@ -128,72 +128,100 @@ __device__ __forceinline__ void v_pairs(const uint32_t (&a)[N], const uint32_t (
 }
 
 // ------------------------------------------------------------- row sources
-// row(slot) = row, relative to the bases handed to the warp, of key slot
-// 0..n-1 of its list, -1 if that slot is masked or out of range.
-// run(slot, N) = row of `slot` if the N slots from there (a multiple of N) all count and
-// lie in consecutive rows, else -1 (the caller then asks for each).
+// A source says which keys a warp's steps of NK slots hold, in two parts, so that what the
+// first one loads is not needed at once:
+//   load(step): a word that the lane needs for it (an index entry, a tile);
+//   key(word, step): the logical key of the lane's slot, -1 if that slot is masked or
+//     out of range; where runs() holds, of the step's first slot: the step's slots are
+//     consecutive keys, of which those below limit() count.
+// `pm`: where keys lie; pm.bt null: a contiguous cache, key = row.
 
-// Logical keys 0 .. n - 1 through the block table.
-struct QPagedRange {
+// Logical keys 0 .. n - 1.
+template <int NK>
+struct QRange {
     int n;
     PageMap pm;
-    __device__ __forceinline__ int row(int slot) const { return slot < n ? pm.row(slot) : -1; }
-    __device__ __forceinline__ int run(int slot, int N) const {
-        return slot + N > n || pm.page_size % N ? -1 : pm.row(slot);
-    }
+    __device__ __forceinline__ bool runs() const { return true; }
+    __device__ __forceinline__ int limit() const { return n; }
+    __device__ __forceinline__ int load(int) const { return 0; }
+    __device__ __forceinline__ int key(int, int step) const { return step * NK; }
 };
-// Entries of an index row (token mode: keys; block mode: blocks clipped to
-// keys <= t), through the block table if there is one.
+// Entries of an index row (token mode, B = 1: keys; block mode: blocks clipped to
+// keys <= t).
+template <int NK>
 struct QIndex {
     const int32_t* ids;
-    int n, B, t;
-    bool paged, runs;  // runs: every NK slots from a multiple of NK may be consecutive rows
+    int n, B, t, top;
+    uint32_t per, inv;  // where runs(): steps of a block, and 2^32 / per rounded up
     PageMap pm;
-    __device__ __forceinline__ int row(int slot) const {
-        if (slot >= n) return -1;
-        int key;
-        if (B == 1) {
-            key = __ldg(ids + slot);
-            if (key < 0 || key > t) { set_status(HS_ERR_BOUNDS); return -1; }
-        } else {
-            const int jb = slot / B;
-            const int id = __ldg(ids + jb);
-            if (id < 0 || id > t / B) { set_status(HS_ERR_BOUNDS); return -1; }
-            key = id * B + (slot - jb * B);
-            if (key > t) return -1;
-        }
-        return paged ? pm.row(key) : key;
+    __device__ __forceinline__ QIndex(const int32_t* ids_, int n_, int B_, int t_, const PageMap& pm_)
+        : ids(ids_), n(n_), B(B_), t(t_), top(t_ / B_), pm(pm_) {
+        per = B % NK == 0 ? B / NK : 0;
+        inv = per > 1 ? 0xffffffffu / per + 1 : 0;
     }
-    __device__ __forceinline__ int run(int slot, int N) const {
-        if (!runs || slot + N > n) return -1;
-        const int jb = slot / B;
-        const int id = __ldg(ids + jb);
-        if (id < 0 || id > t / B) return -1;  // row() reports it
-        const int key = id * B + (slot - jb * B);
-        if (key + N - 1 > t) return -1;
-        return paged ? pm.row(key) : key;
+    __device__ __forceinline__ bool runs() const { return per != 0; }
+    __device__ __forceinline__ int limit() const { return t + 1; }
+    // the block of a run's step (exact for steps < 2^32 / per)
+    __device__ __forceinline__ uint32_t block(int step) const {
+        return per == 1 ? step : __umulhi(step, inv);
+    }
+    __device__ __forceinline__ int slot(int step) const {
+        return step * NK + (int)(threadIdx.x & (NK - 1));
+    }
+    __device__ __forceinline__ int load(int step) const {
+        if (runs()) return step * NK < n ? __ldg(ids + block(step)) : 0;
+        const int s = slot(step);
+        return s < n ? __ldg(ids + (B == 1 ? s : s / B)) : 0;
+    }
+    __device__ __forceinline__ int key(int id, int step) const {
+        if (!runs() && slot(step) >= n) return -1;
+        if (id < 0 || id > top) { set_status(HS_ERR_BOUNDS); return -1; }
+        if (B == 1) return id;
+        const int k = id * B + (runs() ? (int)(step - block(step) * per) * NK : slot(step) % B);
+        return k <= t ? k : -1;
     }
 };
-// The place of a step of NK slots: a run's first row, or this lane's row (lane % NK).
+// A step's keys found: a row (contiguous cache) or an offset in page `page`; the first
+// one's for a run.  -1: none.
 struct QPlace {
-    int row;
+    int at, page;
     bool run;
 };
 template <int NK, class Src>
-__device__ __forceinline__ QPlace place_of(const Src& src, int step, int n_steps) {
-    if (step >= n_steps) return QPlace{-1, false};
-    const int r = src.run(step * NK, NK);
-    if (r >= 0) return QPlace{r, true};
-    return QPlace{src.row(step * NK + (int)(threadIdx.x & (NK - 1))), false};
+__device__ __forceinline__ QPlace find(const Src& src, int word, int step, int n_steps) {
+    QPlace p{-1, 0, false};
+    if (step >= n_steps) return p;
+    int k = src.key(word, step);
+    if (src.runs() && k >= 0) {
+        p.run = k + NK <= src.limit();
+        if (src.pm.bt) p.run = p.run && src.pm.page_size % NK == 0 && k % NK == 0;
+        if (!p.run) {
+            k += threadIdx.x & (NK - 1);
+            if (k >= src.limit()) k = -1;
+        }
+    }
+    if (src.pm.bt && k >= 0) {
+        const int lp = k / src.pm.page_size;
+        p.page = lp < src.pm.max_pages ? __ldg(src.pm.bt + lp) : -1;
+        k -= lp * src.pm.page_size;
+    }
+    p.at = k;
+    return p;
+}
+// The row, relative to the warp's bases, -1 if none or on a bad page.
+__device__ __forceinline__ int row_of(const PageMap& pm, const QPlace& p) {
+    if (!pm.bt || p.at < 0) return p.at;
+    if (p.page < 0 || p.page >= pm.n_pages) { set_status(HS_ERR_BOUNDS); return -1; }
+    return (p.page * pm.hkv + pm.u) * pm.page_size + p.at;
 }
 
 // -------------------------------------------------------------- ring of rows
 // A warp's stages.  K only: the V half is neither filled nor reserved.
-template <int D, int F, bool kV, int kStages>
+template <int D, int F, bool kV, int kStages, int kKeys = QRow<D, F>::kBytes <= 64 ? 32 : 16>
 struct QRing {
     using R = QRow<D, F>;
     static constexpr int RB = R::kBytes;
-    static constexpr int NK = RB <= 64 ? 32 : 16;        // keys of a stage
+    static constexpr int NK = kKeys, kDepth = kStages;   // keys of a stage; stages
     static constexpr int kKeyBytes = NK * RB, kHalf = kKeyBytes + NK * 4;
     static constexpr int kStage = kHalf * (kV ? 2 : 1);  // codes, entries; K, then V
     static constexpr int kBytes = kStages * (kStage + 16);
@@ -235,46 +263,47 @@ struct QRing {
     }
 
     // Starts the copies of a step.
-    __device__ __forceinline__ void fill(int s, const QuantCache& c, const QPlace& at) const {
+    // row: the lane's, or the first one's of a run (-1: a run on a bad page).
+    __device__ __forceinline__ void fill(int s, const QuantCache& c, int row, bool run) const {
         const int lane = threadIdx.x & 31;
         const uint32_t st = stage(s);
         uint32_t live = 0xffffffffu;
-        if (at.run) {  // consecutive bytes
-            const uint8_t* kp = c.kc + (size_t)at.row * RB + lane * 16;
-            const uint8_t* vp = c.vc + (size_t)at.row * RB + lane * 16;
+        if (run && row >= 0) {  // consecutive bytes
+            const uint8_t* kp = c.kc + (size_t)row * RB + lane * 16;
+            const uint8_t* vp = c.vc + (size_t)row * RB + lane * 16;
 #pragma unroll
             for (int i = 0; i < NK / PASS; ++i) {
                 copy16(st + k_dst(i), kp + i * 512);
                 if constexpr (kV) copy16(st + v_to + i * 512, vp + i * 512);
             }
             if (NK == 32 || lane < NK) {
-                copy4(st + e_to, c.ks + (size_t)at.row + lane);
-                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (size_t)at.row + lane);
+                copy4(st + e_to, c.ks + (size_t)row + lane);
+                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (size_t)row + lane);
             }
-        } else if ((live = __ballot_sync(0xffffffffu, at.row >= 0)) == 0xffffffffu) {
+        } else if ((live = __ballot_sync(0xffffffffu, row >= 0)) == 0xffffffffu) {
 #pragma unroll
             for (int i = 0; i < NK / PASS; ++i) {
-                const uint32_t r = __shfl_sync(0xffffffffu, at.row, lane / CH + i * PASS);
+                const uint32_t r = __shfl_sync(0xffffffffu, row, lane / CH + i * PASS);
                 const size_t off = (size_t)r * RB + (lane % CH) * 16;
                 copy16(st + k_dst(i), c.kc + off);
                 if constexpr (kV) copy16(st + v_to + i * 512, c.vc + off);
             }
             if (NK == 32 || lane < NK) {
-                copy4(st + e_to, c.ks + (uint32_t)at.row);
-                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (uint32_t)at.row);
+                copy4(st + e_to, c.ks + (uint32_t)row);
+                if constexpr (kV) copy4(st + kHalf + e_to, c.vs + (uint32_t)row);
             }
         } else {  // rows that do not count are zeros
 #pragma unroll
             for (int i = 0; i < NK / PASS; ++i) {
-                const int r = __shfl_sync(0xffffffffu, at.row, lane / CH + i * PASS);
+                const int r = __shfl_sync(0xffffffffu, row, lane / CH + i * PASS);
                 const size_t off = r >= 0 ? (size_t)r * RB + (lane % CH) * 16 : 0;
                 cp_async16(st + k_dst(i), c.kc + off, r >= 0);
                 if constexpr (kV) cp_async16(st + v_to + i * 512, c.vc + off, r >= 0);
             }
             if (NK == 32 || lane < NK) {
-                const size_t off = at.row >= 0 ? (size_t)at.row : 0;
-                cp_async4(st + e_to, c.ks + off, at.row >= 0);
-                if constexpr (kV) cp_async4(st + kHalf + e_to, c.vs + off, at.row >= 0);
+                const size_t off = row >= 0 ? (size_t)row : 0;
+                cp_async4(st + e_to, c.ks + off, row >= 0);
+                if constexpr (kV) cp_async4(st + kHalf + e_to, c.vs + off, row >= 0);
             }
         }
         if (lane == 0)
@@ -525,8 +554,8 @@ struct QQuery {
 };
 
 struct NoMaxima {
-    template <int NH>
-    __device__ __forceinline__ void operator()(int, const float2 (&)[NH]) const {}
+    template <int NG, int NH>
+    __device__ __forceinline__ void operator()(int, const float2 (&)[NG][NH]) const {}
 };
 
 template <int D, int F, int NH, int kStages, bool kSharedQ = false>
@@ -596,15 +625,15 @@ struct QAttend {
         }
     }
 
-    // One stage's keys.  maxima(step, .): the largest logits (log2 domain) of the lane's
-    // keys, heads 8 n + 2 t, + 1.
+    // One stage's keys.  maxima(step, .): of each 16-key group the largest logits (log2
+    // domain) of the lane's two keys, heads 8 n + 2 t, + 1.
     template <class Maxima>
     __device__ __forceinline__ void step(const Ring& ring, uint32_t st, uint32_t live, int at,
                                          const Maxima& maxima) {
         float2 x[NG][2][NH];
         q.logits(x, ring, st, live);
         uint32_t ent[NG][2];
-        float2 mx[NH];
+        float2 mx[NH], gm[NG][NH];
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -615,18 +644,16 @@ struct QAttend {
         bool grow = big > up;
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            float2 v = x[0][0][n];
-            if constexpr (NG == 2) {
-                v.x = fmaxf(tc::max3f(v.x, x[0][1][n].x, x[1][0][n].x), x[1][1][n].x);
-                v.y = fmaxf(tc::max3f(v.y, x[0][1][n].y, x[1][0][n].y), x[1][1][n].y);
-            } else {
-                v.x = fmaxf(v.x, x[0][1][n].x);
-                v.y = fmaxf(v.y, x[0][1][n].y);
-            }
-            mx[n] = fmul2(v, q.kf[n]);
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+                gm[i][n] = fmul2(make_float2(fmaxf(x[i][0][n].x, x[i][1][n].x),
+                                             fmaxf(x[i][0][n].y, x[i][1][n].y)), q.kf[n]);
+            mx[n] = gm[0][n];
+            if constexpr (NG == 2)
+                mx[n] = make_float2(fmaxf(mx[n].x, gm[1][n].x), fmaxf(mx[n].y, gm[1][n].y));
             grow |= mx[n].x > m[n].x + 14.f || mx[n].y > m[n].y + 14.f;
         }
-        maxima(at, mx);
+        maxima(at, gm);
         if (__any_sync(0xffffffffu, grow)) rescale(mx, big);
         const float down = up == 0.f ? 0.f : __uint_as_float(0x7f000000u - __float_as_uint(up));
         float2 nm[NH];
@@ -674,24 +701,24 @@ struct QAttend {
     template <class Src, class Maxima>
     __device__ __forceinline__ void run(const Ring& ring, const QuantCache& c, const Src& src,
                                         int first, int stride, int n_steps, const Maxima& maxima) {
-        // copies run kStages - 1 steps ahead, the rows' places one more
+        // copies run kStages - 1 steps ahead, the keys' places one more, index entries two
         int ahead = first;
-        QPlace at = place_of<NK>(src, ahead, n_steps);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (ahead < n_steps) ring.fill(i, c, at);
+        QPlace at = find<NK>(src, src.load(first), first, n_steps);
+        int word = first + stride < n_steps ? src.load(first + stride) : 0;
+        auto fill = [&](int s) {
+            if (ahead < n_steps) ring.fill(s, c, row_of(src.pm, at), at.run);
             cp_async_commit();
             ahead += stride;
-            at = place_of<NK>(src, ahead, n_steps);
-        }
+            at = find<NK>(src, word, ahead, n_steps);
+            if (ahead + stride < n_steps) word = src.load(ahead + stride);
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fill(i);
         int s = 0, fs = kStages - 1;
         for (int st = first; st < n_steps; st += stride) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            if (ahead < n_steps) ring.fill(fs, c, at);
-            cp_async_commit();
-            ahead += stride;
-            at = place_of<NK>(src, ahead, n_steps);
+            fill(fs);
             step(ring, ring.stage(s), ring.live(s), st, maxima);
             s = s + 1 == kStages ? 0 : s + 1;
             fs = fs + 1 == kStages ? 0 : fs + 1;

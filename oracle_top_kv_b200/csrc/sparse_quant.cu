@@ -73,11 +73,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, kPerSm<NH> / kRowWarps)
     st.init(q + head0 * D, (size_t)p.t_q * D, p.group, p.scale_log2,
             smem_u32(smem_raw) + kRowWarps * A::Ring::kBytes + (threadIdx.x >> 5) * decltype(st.q)::kBytes);
     const int n = clamp_count(cnt[task], p.ksel) * p.block_size;
-    const QIndex src{idx + (size_t)task * p.ksel, n,           p.block_size,
-                     p.q_offset + j,
-                     p.bt != nullptr,
-                     p.block_size % A::NK == 0 && (p.bt == nullptr || p.page_size % A::NK == 0),
-                     page_map(p, b, u)};
+    const QIndex<A::NK> src{idx + (size_t)task * p.ksel, n, p.block_size, p.q_offset + j,
+                            page_map(p, b, u)};
     st.run(ring, unit_cache<D, F>(p, cache, unit), src, 0, 1, (n + A::NK - 1) / A::NK, NoMaxima{});
     st.finish();
     store_rows<D, NH>(st, p.group, o, lse, head0, (size_t)p.t_q);
@@ -126,8 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
     const typename A::Ring ring{smem_u32(smem_raw) + warp * A::Ring::kBytes};
     if (valid) {
         const int n = clamp_count(cnt[unit], p.ksel);
-        const QIndex src{idx + (size_t)unit * p.ksel, n, 1, L - 1, p.bt != nullptr, false,
-                         page_map(p, b, u)};
+        const QIndex<A::NK> src{idx + (size_t)unit * p.ksel, n, 1, L - 1, page_map(p, b, u)};
         st.run(ring, unit_cache<D, F>(p, cache, unit), src, crank * kWarps + warp, kWarps * csize,
                (n + A::NK - 1) / A::NK, NoMaxima{});
     } else if (crank == 0 && threadIdx.x == 0) {
