@@ -14,7 +14,8 @@
 // by shuffles, kRows rows per thread in flight.  Bound: HBM (2 D bytes in, D / 2 + 4 or
 // D + 4 out per bf16 row).  The quotients that only pick a code are taken with a
 // reciprocal, and by the stated division where that could matter (near a border
-// between two codes): XXX
+// between two codes): 8192 x 4 rows of 128, K and V, 4-bit: 11.8 us written (3.5 TB/s;
+// 16.8 with IEEE division throughout), 5.8 us read back.
 #include <cuda_fp8.h>
 
 #include "hs_common.cuh"
@@ -303,7 +304,8 @@ static void launch_r(const Args& a, bool write, cudaStream_t st) {
 
 template <int D, int F, typename T>
 static void launch_t(const Args& a, bool write, cudaStream_t st) {
-    // several rows per thread once they fill the blocks of a few rows per SM
+    // Several rows per thread once a (sequence, kv head)'s rows fill such a block (8192 x 4
+    // rows: write 16.8 -> 13.5 us, read 8.5 -> 5.8 us, with four); one token's take one.
     if (a.p.t_q >= 4 * (kThreads / (D / 8))) launch_r<D, F, T, 4>(a, write, st);
     else launch_r<D, F, T, 1>(a, write, st);
 }

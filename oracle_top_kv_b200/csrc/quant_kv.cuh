@@ -12,20 +12,23 @@
 // both products run on the codes, exact in fp16, with fp32 accumulators
 // (mma.m16n8k16), and scale and zero are applied to the logits, to P and to one
 // running sum per head.  fp16 rather than bf16, because codes reach it in few
-// instructions: a 4-bit code in a byte, read as e4m3, is the number c 2^-9,
-// exactly, for all of 0..15 (subnormals, then the first binade), so both formats use
-// the conversion of e4m3 pairs.  What fp16's range needs:
+// instructions: a 4-bit code in the lowest bits of a half is the number c 2^-24, four
+// bits higher 16 c 2^-24, both exact subnormals, so 8 codes take a shift and four ANDs
+// (the factor 16 of odd elements is taken from q and from the outputs; against the
+// conversion from e4m3 below, which takes seven instructions: 32 sequences of 131072
+// keys, 16 heads, 578 -> 538 us; the error of a logit grew from 2e-6 to 5e-6 at 23);
+// 8-bit codes are converted in pairs.  What fp16's range needs:
 //  - q is scaled by a power of two per head so that max|q| lies in [2^14, 2^15);
-//    a bf16 element is then exact unless it is 2^-29 of the largest or less
-//    (error 2^-39 of the largest);
+//    a bf16 element is then exact unless it is 2^-25 of the largest or less
+//    (error 2^-35 of the largest);
 //  - p_i s_i is taken relative to 2^10 at the running maximum (growing to
 //    2^14 before O is rescaled) and to a power of two above the largest |s_i|
 //    seen, and rounded to fp16: relative 2^-12 for weights down to 2^-24 of the
 //    largest, an absolute 2^-35 of it below.
 // Everything else is fp32.  What bounds the kernels is the issue rate: mma.sync
 // holds its scheduler for 8 cycles (measured alone 8.7 cycles, with 4 FFMAs beside it
-// 12.8, with 8 of them 17), so 16 keys of 128 dims take 256 issue cycles for their
-// 32 MMAs beside some 250 for unpacking, the softmax and the reads.
+// 12.8, with 8 of them 17), so 16 keys of 128 dims and 16 heads take 272 issue cycles
+// for their 32 MMAs beside some 300 for unpacking, the softmax, the maxima and the reads.
 //
 // One warp takes 16 keys at a time: they are the rows of S^T = K Q^T, 8 heads at a
 // time its columns, and O^T = V^T P^T has 16 dimensions at a time as rows (P^T's
@@ -92,23 +95,29 @@ __device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t& lo, uint32_t& hi)
         : "r"(x));
 }
 
-// What a code of 1 counts for in the operands.
-template <int F> constexpr float kCodeUnit = F == HS_KV_INT4 ? 1.f / 512.f : 1.f;
+// What a code of 1 counts for in the operands; a 4-bit code of an odd element for 16 times
+// that.
+template <int F> constexpr float kCodeUnit = F == HS_KV_INT4 ? 1.f / 16777216.f : 1.f;
+template <int F>
+__host__ __device__ constexpr float odd_unit(int odd) { return F == HS_KV_INT4 && odd ? 1.f / 16.f : 1.f; }
 
 // Dimension (of a quarter row) that element e (0: b0 low, 1: b0 high, 2: b1
 // low, 3: b1 high) of k step `ks` holds.
 template <int F>
 __host__ __device__ constexpr int k_dim(int ks, int e) {
-    return F == HS_KV_INT4 ? 8 * (ks >> 1) + (ks & 1) + 2 * e : 4 * ks + e;
+    return F == HS_KV_INT4 ? 8 * (ks >> 1) + (ks & 1) + 4 * (e & 1) + (e & 2) : 4 * ks + e;
 }
 
 // B fragment (b0, b1) of k step `ks` from a lane's quarter of a K row.
 template <int F, int N>
 __device__ __forceinline__ void k_frag(const uint32_t (&w)[N], int ks, uint32_t& b0, uint32_t& b1) {
-    if constexpr (F == HS_KV_INT4)
-        e4m3_f16((ks & 1 ? w[ks >> 1] >> 4 : w[ks >> 1]) & 0x0f0f0f0fu, b0, b1);
-    else
+    if constexpr (F == HS_KV_INT4) {
+        const uint32_t mask = ks & 1 ? 0x00f000f0u : 0x000f000fu;
+        b0 = w[ks >> 1] & mask;
+        b1 = (w[ks >> 1] >> 8) & mask;
+    } else {
         e4m3_f16(w[ks], b0, b1);
+    }
 }
 
 // Pairs (a[j + i], b[j + i]), i = 0..3, of a lane's eighths of two V rows, j a
@@ -117,10 +126,13 @@ template <int F, int N>
 __device__ __forceinline__ void v_pairs(const uint32_t (&a)[N], const uint32_t (&b)[N], int j,
                                         uint32_t (&p)[4]) {
     if constexpr (F == HS_KV_INT4) {
-        // bytes (a, b, a, b) of two neighbouring bytes of each row
-        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7362 : 0x5140);
-        e4m3_f16(x & 0x0f0f0f0fu, p[0], p[2]);
-        e4m3_f16((x >> 4) & 0x0f0f0f0fu, p[1], p[3]);
+        // two neighbouring bytes of each row
+        const uint32_t x = __byte_perm(a[j >> 3], b[j >> 3], (j & 4) ? 0x7632 : 0x5410);
+        const uint32_t y = x >> 8;
+        p[0] = x & 0x000f000fu;
+        p[1] = x & 0x00f000f0u;
+        p[2] = y & 0x000f000fu;
+        p[3] = y & 0x00f000f0u;
     } else {
         e4m3_f16(__byte_perm(a[j >> 2], b[j >> 2], 0x5140), p[0], p[1]);
         e4m3_f16(__byte_perm(a[j >> 2], b[j >> 2], 0x7362), p[2], p[3]);
@@ -455,8 +467,10 @@ struct QQuery {
             // 2^(14 - exponent); the exponent is held above -100, where q still fits
             const int ex = max((int)(__float_as_uint(amax) >> 23), 27) - 127;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            const float k = fmaxf(scale_log2 / kCodeUnit<F> *
-                                      __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f);
+            // held in the normal range: |q| up to 2^117 at the usual scales
+            const float k = fminf(fmaxf(scale_log2 / kCodeUnit<F> *
+                                            __uint_as_float((uint32_t)(127 - 14 + ex) << 23), 1.2e-38f),
+                                  3.4e38f);
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) {
@@ -470,7 +484,8 @@ struct QQuery {
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = pack_f16(x[k_dim<F>(ks, 2 * e)], x[k_dim<F>(ks, 2 * e + 1)]);
+                    const uint32_t w = pack_f16(x[k_dim<F>(ks, 2 * e)] * odd_unit<F>(ks & 1),
+                                                x[k_dim<F>(ks, 2 * e + 1)] * odd_unit<F>(ks & 1));
                     if constexpr (kShared)
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + (ks * NH + n) * 256 + 4 * e),
                                      "r"(w) : "memory");
@@ -785,7 +800,8 @@ struct QAttend {
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[j][n][e] = fmaf(o[j][n][e], up / kCodeUnit<F>, e & 1 ? zacc[n].y : zacc[n].x);
+                    o[j][n][e] = fmaf(o[j][n][e] * (odd_unit<F>(e >> 1) / kCodeUnit<F>), up,
+                                      e & 1 ? zacc[n].y : zacc[n].x);
         }
     }
 

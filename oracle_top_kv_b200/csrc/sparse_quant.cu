@@ -16,8 +16,10 @@ namespace sq {
 constexpr int kWarps = 4;      // of a decode CTA
 constexpr int kRowWarps = 1;   // of a prefill CTA: the warps work alone
 constexpr int kStages = 2;
-// 16 heads: Q in shared memory lets three CTAs share an SM without spills (2048 rows x 4
-// groups x 1024 keys: XXX us against YYY with Q in registers).
+// 16 heads: Q in shared memory leaves registers for 12 warps on an SM in place of 8 (4-bit,
+// 2048 rows x 4 groups x 1024 keys: 388 us against 483 with Q in registers, when this was
+// chosen; 312 us now).  8 heads: Q in registers, 16 warps (8-bit, 1000 rows x 8 groups of
+// 4 heads x 16 blocks of 64: 300 us, 7.2 TB/s of rows, which come from L2).
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2>;
 template <int D, int F, int NH>
 constexpr size_t kWarpBytes =  // a warp's ring and query
