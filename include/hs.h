@@ -318,7 +318,8 @@ hs_status hs_decode_step_paged(const hs_params* p, const hs_pages* pages, int32_
  *   k_scale, v_scale   [batch][hkv][t_kv][2] bf16
  * or, with `pages` (NULL: contiguous), pools [n_pages][hkv][page_size][..] with
  * the rules of hs_sparse_attn_reuse_paged (p->t_kv = max_pages * page_size).
- * Groups of up to 16 heads, head_dim 64 or 128; queries and outputs bf16.
+ * Groups of up to 16 heads, head_dim 64 or 128 (else HS_ERR_UNSUPPORTED);
+ * queries and outputs bf16; t_kv up to 2^31 - 4097.
  */
 typedef enum { HS_KV_INT4 = 0, HS_KV_FP8 = 1 } hs_kv_format;
 
@@ -339,7 +340,8 @@ typedef struct {
  * seq_len, n_new: DEVICE int32 [batch]; NULL: p->q_offset + t_q, and t_q, for
  * every sequence.  A sequence with n_new outside 0..t_q or seq_len outside
  * n_new..t_kv, or a row on a bad page, is skipped and sets HS_ERR_BOUNDS.
- * Only batch, hq, hkv, head_dim, t_q, t_kv, q_offset and dtype of p are used.
+ * Only batch, hq, hkv, head_dim, t_q, t_kv, q_offset and dtype of p are used;
+ * the others have to be valid.
  */
 hs_status hs_kv_quant_write(const hs_params* p, const hs_kv_quant* kv, const hs_pages* pages,
                             const void* k, const void* v, const int32_t* seq_len,

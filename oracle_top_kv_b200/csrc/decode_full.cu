@@ -504,35 +504,6 @@ __global__ void __launch_bounds__(kSelectThreads)
     if (threadIdx.x == 0) cnt[unit] = n_out;
 }
 
-// Merges the slices' candidates of the split selector into the index rows.
-static cudaError_t launch_select_merge(const KParams& p, const DecodeWs& w,
-                                       const int32_t* seq_len, int32_t* idx, int32_t* cnt,
-                                       float* sel, cudaStream_t st) {
-    cudaError_t e;
-    const uint64_t* cand = w.cand;
-    const int* cand_n = w.cand_n;
-    int n_src = w.n_sel;
-    if (w.n_grp > 0) {  // many slices: fold groups of them on more CTAs first
-        const size_t sg = sizeof(uint64_t) * (kSelGroup * kSelMaxRanked + kSelMaxRanked);
-        e = cudaFuncSetAttribute(decode_select_group_kernel,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sg);
-        if (e != cudaSuccess) return e;
-        decode_select_group_kernel<<<p.batch * p.hkv * w.n_grp, kSelectThreads, sg, st>>>(
-            p, seq_len, w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        cand = w.cand2;
-        cand_n = w.cand2_n;
-        n_src = w.n_grp;
-    }
-    const size_t s2 = sizeof(uint64_t) * (kMergeCap + kSelMaxRanked);
-    e = cudaFuncSetAttribute(decode_select_merge_kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
-    if (e != cudaSuccess) return e;
-    decode_select_merge_kernel<<<p.batch * p.hkv, kSelectThreads, s2, st>>>(
-        p, seq_len, w, cand, cand_n, n_src, idx, cnt, sel);
-    return cudaGetLastError();
-}
-
 template <int D>
 static cudaError_t launch_decode_full_t(const KParams& p, const void* q, const void* kc,
                                         const void* vc, const int32_t* seq_len, int32_t* idx,
@@ -569,7 +540,28 @@ static cudaError_t launch_decode_full_t(const KParams& p, const void* q, const v
         decode_select_split_kernel<<<p.batch * p.hkv * w.n_sel, kSelectThreads, s1, st>>>(
             p, seq_len, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        return launch_select_merge(p, w, seq_len, idx, cnt, sel, st);
+        const uint64_t* cand = w.cand;
+        const int* cand_n = w.cand_n;
+        int n_src = w.n_sel;
+        if (w.n_grp > 0) {  // many slices: fold groups of them on more CTAs first
+            const size_t sg = sizeof(uint64_t) * (kSelGroup * kSelMaxRanked + kSelMaxRanked);
+            e = cudaFuncSetAttribute(decode_select_group_kernel,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sg);
+            if (e != cudaSuccess) return e;
+            decode_select_group_kernel<<<p.batch * p.hkv * w.n_grp, kSelectThreads, sg, st>>>(
+                p, seq_len, w);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            cand = w.cand2;
+            cand_n = w.cand2_n;
+            n_src = w.n_grp;
+        }
+        const size_t s2 = sizeof(uint64_t) * (kMergeCap + kSelMaxRanked);
+        e = cudaFuncSetAttribute(decode_select_merge_kernel,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2);
+        if (e != cudaSuccess) return e;
+        decode_select_merge_kernel<<<p.batch * p.hkv, kSelectThreads, s2, st>>>(
+            p, seq_len, w, cand, cand_n, n_src, idx, cnt, sel);
+        return cudaGetLastError();
     }
     const size_t sel_smem = BlockTopK::smem_bytes(Kc, kSelectThreads);
     e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -247,9 +247,9 @@ __device__ __forceinline__ T* cluster_ptr(T* a, int rank) {
 // of the cluster are >= t (fewer than k + 1 keys: the least): get(0) .. get(n - 1) are
 // this CTA's.  All threads of all CTAs call; all get the result.  Range bucket select as
 // cta_kth_largest, which ends as soon as the bucket that holds the k-th largest fits
-// into the slack; each CTA counts, CTA 0 sums.
+// into the slack; each CTA counts its own keys and reads the others' counts.
 struct ThresholdSmem {
-    uint32_t hist[2][256];
+    alignas(16) uint32_t hist[2][256];
     unsigned long long lo, hi;
     unsigned long long nlo, nhi;
     int need, done;
@@ -257,8 +257,8 @@ struct ThresholdSmem {
 template <typename Get>
 __device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, int C, int rank) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-    ThresholdSmem* root = C > 1 ? cluster_ptr(&sh, 0) : &sh;
     auto sync = [&] {
+        __syncwarp();  // the barrier takes whole warps
         if (C > 1) cluster_sync_all();
         else __syncthreads();
     };
@@ -276,14 +276,20 @@ __device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, 
     }
     if (tid == 0) { sh.lo = ~0ull; sh.hi = 0ull; }
     for (int x = tid; x < 512; x += nt) (&sh.hist[0][0])[x] = 0u;
-    sync();
+    __syncthreads();
     if (lane == 0 && mn <= mx) {
-        atomicMin(&root->lo, (unsigned long long)mn);
-        atomicMax(&root->hi, (unsigned long long)mx);
+        atomicMin(&sh.lo, (unsigned long long)mn);
+        atomicMax(&sh.hi, (unsigned long long)mx);
     }
     sync();
-    uint64_t lo = *(volatile unsigned long long*)&root->lo;
-    uint64_t hi = *(volatile unsigned long long*)&root->hi;
+    uint64_t lo = ~0ull, hi = 0ull;
+    for (int r = 0; r < C; ++r) {
+        const ThresholdSmem* s = C > 1 ? cluster_ptr(&sh, r) : &sh;
+        const uint64_t a = *(volatile const unsigned long long*)&s->lo;
+        const uint64_t b = *(volatile const unsigned long long*)&s->hi;
+        lo = a < lo ? a : lo;
+        hi = b > hi ? b : hi;
+    }
     int need = k;
     for (int pass = 0; pass < 9 && lo < hi; ++pass) {
         const int h = pass & 1, shift = max(0, top_bit64(hi - lo) - 7);
@@ -292,20 +298,20 @@ __device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, 
             if (v >= lo && v <= hi) atomicAdd(&sh.hist[h][(uint32_t)((v - lo) >> shift)], 1u);
         }
         sync();
-        if (C > 1) {
-            if (rank != 0)
-                for (int x = tid; x < 256; x += nt)
-                    if (sh.hist[h][x]) atomicAdd(&root->hist[h][x], sh.hist[h][x]);
-            cluster_sync_all();
-        }
         if (tid < 32) {
-            uint32_t c[8], s = 0;
+            uint32_t c[8] = {};  // lane l owns buckets 255 - 8l .. 248 - 8l, from the top
+            for (int r = 0; r < C; ++r) {
+                const ThresholdSmem* from = C > 1 ? cluster_ptr(&sh, r) : &sh;
+                const uint4* at = reinterpret_cast<const uint4*>(&from->hist[h][248 - 8 * lane]);
+                const uint4 a = at[1], b = at[0];
+                const uint32_t v[8] = {a.w, a.z, a.y, a.x, b.w, b.z, b.y, b.x};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[j] = *(volatile uint32_t*)&root->hist[h][255 - 8 * lane - j];
-                s += c[j];
+                for (int j = 0; j < 8; ++j) c[j] += v[j];
             }
-            uint32_t incl = s;  // lane l owns buckets 255 - 8l .. 248 - 8l, from the top
+            uint32_t s = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += c[j];
+            uint32_t incl = s;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -324,7 +330,7 @@ __device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, 
                 sh.done = (int)(above + c[j]) <= need + kSlack;
             }
         }
-        // the other histogram was last read before the sync above
+        // the other histogram was last read, by other CTAs too, before the sync above
         for (int x = tid; x < 256; x += nt) sh.hist[h ^ 1][x] = 0u;
         __syncthreads();
         lo = sh.nlo;
@@ -334,7 +340,7 @@ __device__ uint64_t cluster_threshold(Get get, int n, int k, ThresholdSmem& sh, 
         __syncthreads();  // read by all before the next pass writes
         if (done) break;
     }
-    if (C > 1) cluster_sync_all();  // CTA 0 keeps its histograms until all have read them
+    sync();  // the histograms stay until all have read them
     return lo;
 }
 
@@ -636,7 +642,8 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         const int full = lo / kSub;  // tiles of ranked keys only; tile `full` has some if lo % kSub
         // this CTA's tiles: chunks of 32, dealt out over the cluster
         const int chunks = (full + 31) / 32;
-        const int mine = (chunks > rank ? (chunks - rank - 1) / C + 1 : 0) * 32;
+        const int mine = (chunks > rank ? (chunks - rank - 1) / C + 1 : 0) * 32 -
+                         ((chunks - 1) % C == rank ? chunks * 32 - full : 0);
         auto tile = [&](int i) { return ((i >> 5) * C + rank) * 32 + (i & 31); };
         auto offer = [&](int key, float v) {
             const uint64_t c = sel_key(v, (uint32_t)key);
@@ -663,7 +670,6 @@ __global__ void __launch_bounds__(kSelThreads, 1)
             uint32_t* bits = mine <= kBoundCap ? reinterpret_cast<uint32_t*>(smem_raw)
                                                : ws.bits + (size_t)unit * (ws.tiles + kBitsPad) +
                                                      (size_t)rank * ((chunks + C - 1) / C) * 32;
-            // a CTA may hold up to 31 places past its tiles: they rank last
             constexpr int U = 2, Q4 = 2 * NH;  // tiles in flight per thread, float4 of a tile
             for (int i0 = tid; i0 < mine; i0 += U * kSelThreads) {
                 float4 a[U][Q4];
@@ -672,7 +678,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                     const int i = i0 + k * kSelThreads, x = tile(i);
 #pragma unroll
                     for (int q4 = 0; q4 < Q4; ++q4)
-                        a[k][q4] = i < mine && x < full ? __ldg(tm + (size_t)x * 4 + q4)
+                        a[k][q4] = i < mine ? __ldg(tm + (size_t)x * 4 + q4)
                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                         for (int e = 0; e < 4; ++e)
                             v = fmaxf(v, __fsub_rn(av[e], s_lse2[4 * q4 + e]));
                     }
-                    bits[i] = tile(i) < full ? float_order(v) : 0u;
+                    bits[i] = float_order(v);
                 }
             }
             __syncthreads();
@@ -699,11 +705,12 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                 if (key(i) >= kth) list[atomicAdd(&s_list, 1)] = tile(i);
             if (tid == 0) {
                 // the bounds and the scores below are the same arithmetic on the same
-                // operands; the step down covers a difference in their last bits
+                // operands; the step down covers a difference in their last bits.  kth may
+                // lie between two keys, and stand for no number.
                 const float th = sel_key_score(kth);
                 float mag = fabsf(th);
                 for (int h = 0; h < g; ++h) mag = fmaxf(mag, fabsf(s_lse2[h]));
-                s_thr = isfinite(mag) ? (uint64_t)float_order(th - 4e-6f * mag) << 32 : 0ull;
+                s_thr = isfinite(th) && isfinite(mag) ? (uint64_t)float_order(th - 4e-6f * mag) << 32 : 0ull;
             }
             __syncthreads();
             if (tid == 0 && rank == 0 && lo % kSub != 0) list[s_list++] = full;
@@ -721,6 +728,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
         }
         if (C > 1) {
             if (tid == 0) s_n = n_best;
+            __syncwarp();
             cluster_sync_all();
             if (rank == 0)
                 for (int r = 1; r < C; ++r) {
@@ -734,6 +742,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                         n_best = Kc;
                     }
                 }
+            __syncwarp();
             cluster_sync_all();  // the others keep their buffers until here
             if (rank != 0) return;
         }

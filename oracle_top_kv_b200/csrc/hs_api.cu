@@ -316,8 +316,9 @@ hs_status resolve_quant(const hs_params* p, const hs_kv_quant* kv, const hs_page
         !ok_ptr(kv->v_scale))
         return HS_ERR_INVALID_ARG;
     if (!mma_shape(*kp)) return HS_ERR_UNSUPPORTED;
-    // tasks of a launch are counted in 31 bits
+    // tasks of a launch are counted in 31 bits, and so are keys, up to a step past the last
     if ((double)kp->batch * kp->hq * kp->t_q >= 2147483648.0) return HS_ERR_INVALID_ARG;
+    if (kp->t_kv > INT32_MAX - 4096) return HS_ERR_INVALID_ARG;
     *c = hs::QuantCache{(const uint8_t*)kv->k_codes, (const uint32_t*)kv->k_scale,
                         (const uint8_t*)kv->v_codes, (const uint32_t*)kv->v_scale};
     return HS_OK;

@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
         }
         reinterpret_cast<float4*>(mine + 32)[e] = a;
     }
+    __syncwarp();  // the barrier takes whole warps
     if (csize > 1) cluster_sync_all();
     else __syncthreads();
     // the cluster's: weights again, then each CTA writes a share of the outputs
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH> / kWarps)
         *reinterpret_cast<uint2*>(o + head0 * D + 4 * e) =
             make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     }
+    __syncwarp();
     if (csize > 1) cluster_sync_all();  // peers keep their shared memory until all have read
 }
 

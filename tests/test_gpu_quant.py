@@ -4,8 +4,8 @@ decode steps and the sparse prefill layer over them.
 Rows are compared with quant_ref (equal codes, scales and zeros); attention is
 compared with the fp64 oracle on the values that the stored codes stand for,
 under the bars of tests/parity.py.  These cover what the kernels round: q and
-the codes enter the products exactly, p_i scale_i is rounded to bf16 (2^-9 of
-each term: against an output of independent terms at most a few 2^-9 of its
+the codes enter the products exactly, p_i scale_i is rounded to fp16 (2^-12 of
+each term: against an output of independent terms at most a few 2^-12 of its
 RMS, below 1.5e-2), the output once more (the half ulp).
 """
 import numpy as np

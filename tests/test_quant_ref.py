@@ -144,3 +144,8 @@ def test_full_step_workspace(lib):
 def test_binding_refuses_unknown_formats():
     with pytest.raises(KeyError):
         hs.make_kv_quant("int3", None, None, None, None)
+
+
+def test_lengths_that_a_step_could_pass_are_refused(lib):
+    p = _p(batch=1, hq=1, hkv=1, head_dim=64, t_kv=2 ** 31 - 4096)
+    assert set(_calls(lib, p, _kv()).values()) == {INV}
