@@ -33,7 +33,10 @@ constexpr int kWarps = 4;
 constexpr int kStages = 2;
 constexpr int kMaxCtas = 640;  // partial slots reserved: at most kMaxCtas + units
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages>;
-// Four-warp CTAs of the full kernel to an SM that the registers are divided for.
+// Four-warp CTAs of the full kernel to an SM that the registers are divided for: 8 heads fit
+// 128 registers (8-bit ragged batch, 32/8 heads: 65 us, 67 with three CTAs), 16 heads take
+// 240 (a third CTA, with Q in shared memory: 581 us against 558 for 32 x 131072 keys).
+// Steps of 16 keys of 128-byte rows: with 32 and three CTAs 66 us against 64.
 template <int NH> constexpr int kPerSm = NH == 1 ? 4 : 2;
 
 constexpr int kSelThreads = 512;
@@ -47,7 +50,8 @@ constexpr int kSlack = 16;
 // Ring of a rescoring warp (some 100 KB for the CTA's 16).
 template <int D, int F> using KeyRing = QRing<D, F, false, 3>;
 // Rounds of rescoring between looks at the number of candidates, where the buffer for
-// that many fits (budgets k - w up to about 3000); else 1.
+// that many fits (budgets k - w up to about 3000); else 1 (at the usual budgets: short
+// caches 16.8 us, with a look a round 22.3; 32 x 131072 keys 104 against 112).
 constexpr int kCheck = 4;
 
 constexpr int kBitsPad = 512;     // the tiles are dealt out in chunks of 32 to up to 8 CTAs
@@ -830,8 +834,9 @@ static cudaError_t launch_t(const KParams& p, const QuantCache& c, const void* q
     if ((e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) !=
         cudaSuccess)
         return e;
-    // clusters as wide as a wave of one CTA per SM allows, while a CTA still
-    // has more than 8 chunks of tiles
+    // Clusters as wide as a wave of one CTA per SM allows, while the capacity gives a CTA
+    // more than 256 steps (one sequence of 2^20 keys: 64 us on 4 x 8 CTAs, 244 on 4; 8-bit
+    // ragged batch of 9 x 8 units: 55 us on pairs, 70 alone).
     int C = 1;
     while (C < 8 && units * C * 2 <= sms && steps / (C * 2) > 256) C *= 2;
     cudaLaunchConfig_t cfg = {};

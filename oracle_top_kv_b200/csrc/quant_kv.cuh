@@ -573,9 +573,10 @@ struct NoMaxima {
     __device__ __forceinline__ void operator()(int, const float2 (&)[NG][NH]) const {}
 };
 
-template <int D, int F, int NH, int kStages, bool kSharedQ = false>
+template <int D, int F, int NH, int kStages, bool kSharedQ = false,
+          int kKeys = QRow<D, F>::kBytes <= 64 ? 32 : 16>
 struct QAttend {
-    using Ring = QRing<D, F, true, kStages>;
+    using Ring = QRing<D, F, true, kStages, kKeys>;
     static constexpr int NK = Ring::NK, NG = NK / 16;
 
     QQuery<D, F, NH, kSharedQ> q;

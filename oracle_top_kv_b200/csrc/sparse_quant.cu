@@ -18,14 +18,17 @@ constexpr int kRowWarps = 1;   // of a prefill CTA: the warps work alone
 constexpr int kStages = 2;
 // 16 heads: Q in shared memory leaves registers for 12 warps on an SM in place of 8 (4-bit,
 // 2048 rows x 4 groups x 1024 keys: 388 us against 483 with Q in registers, when this was
-// chosen; 312 us now).  8 heads: Q in registers, 16 warps (8-bit, 1000 rows x 8 groups of
-// 4 heads x 16 blocks of 64: 300 us, 7.2 TB/s of rows, which come from L2).
-template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2>;
+// chosen; 308 us now).  32 keys a step, of 128-byte rows too, where the work of a step that is
+// not its keys' would weigh twice (8-bit, 1000 rows x 8 groups of 4 heads x 16 blocks of 64:
+// 297 us with 16 keys a step, 222 with 32: 9.8 TB/s of rows, most of which come from L2).
+template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2, 32>;
 template <int D, int F, int NH>
 constexpr size_t kWarpBytes =  // a warp's ring and query
-    QRing<D, F, true, kStages>::kBytes + QQuery<D, F, NH, NH == 2>::kBytes;
-// Warps to an SM that the registers are divided for.
-template <int NH> constexpr int kPerSm = NH == 1 ? 16 : 12;
+    Attend<D, F, NH>::Ring::kBytes + QQuery<D, F, NH, NH == 2>::kBytes;
+// Warps to an SM that the registers are divided for.  8 heads: 14, between few warps and
+// few registers (1000 rows x 8 groups of 4 heads, 1024 keys, at 12, 14, 16 warps: 8-bit
+// blocks 221, 222, 239 us, 4-bit tokens 231, 213, 219, head_dim 64 163, 148, 149).
+template <int NH> constexpr int kPerSm = NH == 1 ? 14 : 12;
 
 // Writes a unit's heads from a warp's finished accumulators.
 template <int D, int NH, class A>
@@ -230,7 +233,8 @@ static cudaError_t launch_decode_t(const KParams& p, const QuantCache& c, const 
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     // Widest cluster (a portable size) whose CTAs still run in one wave, two
-    // to an SM, with a step for every warp.
+    // to an SM, with a step for every warp (8 units of 1152 rows: 8.8 us on clusters of 8,
+    // 19 on one CTA each; 128 units of 1024 rows: 18.4 us on pairs, as on one).
     const int units = p.batch * p.hkv;
     const int steps = (p.ksel + Attend<D, F, NH>::NK - 1) / Attend<D, F, NH>::NK;
     int csize = 1;
