@@ -585,6 +585,7 @@ struct QAttend {
     float o[D / 16][NH][4];
     float2 m[NH];             // p = 2^(logit - m); m lies 10..14 below the running maximum
     float2 l[NH], zacc[NH];   // sums of p and p z over the lane's keys
+    float2 off[NH];           // what recentre() took from the lane's part of O
     float up;                 // power of two above every |scale| seen: O counts in it
 
     __device__ __forceinline__ void init(const __nv_bfloat16* qp, size_t stride, int g,
@@ -594,7 +595,7 @@ struct QAttend {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             m[n] = both(-INFINITY);
-            l[n] = zacc[n] = both(0.f);
+            l[n] = zacc[n] = off[n] = both(0.f);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -634,6 +635,7 @@ struct QAttend {
             m[n].y = moved(m[n].y, mx[n].y, f.y);
             l[n] = fmul2(l[n], f);
             zacc[n] = fmul2(zacc[n], f);
+            off[n] = fmul2(off[n], make_float2(f.x * fo, f.y * fo));
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -713,6 +715,35 @@ struct QAttend {
         }
     }
 
+    // The matrix unit cuts sums off where they lose bits, and 4-bit codes are positive: O
+    // would carry the codes' mean, up to many times what is left of it once the zero points
+    // are in, and lose a little of it each time (131072 keys of equal weight, 886 sums a warp:
+    // outputs 3.1% of their RMS too low).  So every kRecentre steps each head's mean over
+    // the lane's dimensions moves into an fp32 sum of its own.
+    static constexpr int kRecentre = 8;
+    __device__ __forceinline__ void recentre() {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            float2 s = both(0.f);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                s = tc::ffma2(make_float2(o[j][n][2], o[j][n][3]), both(odd_unit<F>(1)),
+                              tc::fadd2(s, make_float2(o[j][n][0], o[j][n][1])));
+            const float2 a = fmul2(s, both(1.f / (D / 8)));
+            off[n] = tc::fadd2(off[n], a);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[j][n][e] = fmaf(e & 1 ? a.y : a.x, -1.f / odd_unit<F>(e >> 1), o[j][n][e]);
+        }
+    }
+    // To be called after the i-th step (from 0) of a run.
+    __device__ __forceinline__ void stepped(int i) {
+        if constexpr (F == HS_KV_INT4)
+            if (i % kRecentre == kRecentre - 1) recentre();
+    }
+
     // Steps first, first + stride, ... below n_steps of a source's list.
     template <class Src, class Maxima>
     __device__ __forceinline__ void run(const Ring& ring, const QuantCache& c, const Src& src,
@@ -730,12 +761,13 @@ struct QAttend {
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) fill(i);
-        int s = 0, fs = kStages - 1;
+        int s = 0, fs = kStages - 1, done = 0;
         for (int st = first; st < n_steps; st += stride) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
             fill(fs);
             step(ring, ring.stage(s), ring.live(s), st, maxima);
+            stepped(done++);
             s = s + 1 == kStages ? 0 : s + 1;
             fs = fs + 1 == kStages ? 0 : fs + 1;
         }
@@ -779,6 +811,7 @@ struct QAttend {
             const int left = n - st * NK;
             const uint32_t live = left >= NK ? (NK == 32 ? 0xffffffffu : 0xffffu) : (1u << left) - 1u;
             step(ring, ring.base + at, live, st, maxima);
+            stepped((st - first) / kStride);
             at = at + Ring::kStage == kEnd ? 0u : at + Ring::kStage;
         }
         cp_async_wait<0>();
@@ -790,6 +823,8 @@ struct QAttend {
     __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
+            // what the lane's dimensions have in common
+            float2 base;
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) {
                 l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, w);
@@ -797,12 +832,14 @@ struct QAttend {
                 zacc[n].x += __shfl_xor_sync(0xffffffffu, zacc[n].x, w);
                 zacc[n].y += __shfl_xor_sync(0xffffffffu, zacc[n].y, w);
             }
+            base.x = fmaf(off[n].x * (1.f / kCodeUnit<F>), up, zacc[n].x);
+            base.y = fmaf(off[n].y * (1.f / kCodeUnit<F>), up, zacc[n].y);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     o[j][n][e] = fmaf(o[j][n][e] * (odd_unit<F>(e >> 1) / kCodeUnit<F>), up,
-                                      e & 1 ? zacc[n].y : zacc[n].x);
+                                      e & 1 ? base.y : base.x);
         }
     }
 

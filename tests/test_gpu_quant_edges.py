@@ -345,3 +345,76 @@ def test_tensors_that_the_binding_refuses(monkeypatch):
     monkeypatch.setattr(hs, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="current CUDA device"):
         hs.hs_kv_quant_write(p, c.kv, None, k, k, stream=0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hq", [5, 16])
+def test_any_codes_and_entries(fmt, hq):
+    """Caches that hs_kv_quant_write would not write: every code, scales of both signs and zero,
+    zero points in both formats; and a scale argument of the caller's."""
+    p = _params(2, hq, 1, 128, 1, 1500, k=80, window=16, scale=0.03)
+    c = Cache(p, fmt)
+    g = torch.Generator().manual_seed(120)
+    for codes, entry in (c.t[:2], c.t[2:]):
+        x = torch.randint(0, 256, codes.shape, generator=g)
+        if fmt == "fp8":
+            x = torch.where(x % 128 == 127, x - 1, x)  # not NaN
+        codes.copy_(x.to(torch.uint8))
+        e = torch.randn(entry.shape, generator=g) * torch.tensor([0.2 if fmt == "int4" else 0.005, 0.5])
+        e[:, :, ::7, 0] = 0
+        entry.copy_(e.bfloat16())
+    q = _randn(2, hq, 1, 128, seed=121)
+    seq = torch.tensor([1500, 700], dtype=torch.int32, device=DEV)
+    o, lse, idx, cnt, _ = _full(p, c, q, seq)
+    os_, ls = torch.empty_like(o), torch.empty_like(lse)
+    hs.hs_decode_step_quant(p, c.kv, None, hs.HS_DECODE_SPARSE, q, seq, idx, cnt, os_, ls)
+    assert hs.hs_device_status() == 0
+    kd, vd = c.values()
+    for b, L in enumerate(seq.tolist()):
+        a = 0.03 * (q[b, :, 0].double().cpu().numpy() @ kd[b, 0, :L].T)
+        l = np.logaddexp.reduce(a, 1)
+        w = np.exp(a - l[:, None])
+        P.check_lse(lse.cpu().double().numpy()[b, :, 0], l, "bf16", "lse")
+        # p scale is rounded to fp16, 2^-12 of each term p scale c; the output to bf16
+        z = c.t[3][b, 0, :, 1].double().cpu().numpy()[:, None]
+        size = np.abs(vd[b, 0] - z) + np.abs(z)
+        mag = w @ size[:L]
+        want = w @ vd[b, 0, :L]
+        err = np.abs(P.f64(o)[b, :, 0] - want)
+        assert (err <= 2.0 ** -11 * mag + 2.0 ** -8 * np.abs(want) + 1e-6).all()
+        got = idx[b, 0].cpu().numpy()
+        score = (a - l[:, None]).max(0)
+        kth = np.sort(score[:L - 16])[-64]
+        assert int(cnt[b, 0]) == 80 and (score[got[:64]] >= kth - P.INDEX_REL).all()
+        at = a[:, got]
+        P.check_lse(ls.cpu().double().numpy()[b, :, 0], np.logaddexp.reduce(at, 1), "bf16", "sparse lse")
+        w = np.exp(at - np.logaddexp.reduce(at, 1)[:, None])
+        err = np.abs(P.f64(os_)[b, :, 0] - w @ vd[b, 0, got])
+        assert (err <= 2.0 ** -11 * (w @ size[got]) + 2.0 ** -8 * np.abs(w @ vd[b, 0, got]) + 1e-6).all()
+
+
+def test_long_diffuse_attention_in_4_bits():
+    """131072 keys of nearly equal weight, many to a warp: what is left of the codes' mean once
+    the zero points are in is a 900th of it, and is held to the usual bar."""
+    b, hq, hkv, d, T = 32, 64, 4, 128, 131072
+    p = _params(b, hq, hkv, d, 1, T, k=64, window=8)
+    gen = torch.Generator(DEV).manual_seed(130)
+    t = hs.kv_quant_cache(p, "int4", DEV)
+    for codes, entry in (t[:2], t[2:]):
+        codes.random_(0, 256, generator=gen)
+        entry[..., 0], entry[..., 1] = 0.3125, -0.3125 * 7.5
+    q = _randn(b, hq, 1, d, seed=131, std=0.3)
+    seq = torch.full((b,), T, dtype=torch.int32, device=DEV)
+    idx, cnt, o, lse, _ = _decode_outputs(p)
+    hs.hs_decode_step_quant(p, hs.make_kv_quant("int4", *t), None, hs.HS_DECODE_FULL_INDEX, q, seq,
+                            idx, cnt, o, lse, None, hs.workspace(p, hs.HS_WS_DECODE_FULL_QUANT))
+    assert hs.hs_device_status() == 0
+    for i, u in ((0, 0), (13, 2), (31, 3)):
+        k, v = ((torch.stack([c[i, u] & 15, c[i, u] >> 4], -1).flatten(1).double() - 7.5) * 0.3125
+                for c in (t[0], t[2]))
+        heads = slice(u * 16, (u + 1) * 16)
+        a = q[i, heads, 0].double() @ k.T / d ** 0.5
+        l = torch.logsumexp(a, -1)
+        want = torch.exp(a - l[:, None]) @ v
+        P.check_o(P.f64(o[i, heads, 0]), P.f64(want), "bf16", "o")
+        P.check_lse(P.f64(lse[i, heads, 0]), P.f64(l), "bf16", "lse")
