@@ -28,7 +28,8 @@
 // Everything else is fp32.  What bounds the kernels is the issue rate: mma.sync
 // holds its scheduler for 8 cycles (measured alone 8.7 cycles, with 4 FFMAs beside it
 // 12.8, with 8 of them 17), so 16 keys of 128 dims and 16 heads take 272 issue cycles
-// for their 32 MMAs beside some 300 for unpacking, the softmax, the maxima and the reads.
+// for their 32 MMAs beside some 320 for unpacking, the softmax, the maxima and the reads
+// (32 sequences of 131072 keys, 16 heads of 128: 553 us, 4.1 TB/s of cache).
 //
 // One warp takes 16 keys at a time: they are the rows of S^T = K Q^T, 8 heads at a
 // time its columns, and O^T = V^T P^T has 16 dimensions at a time as rows (P^T's
@@ -635,7 +636,7 @@ struct QAttend {
             m[n].y = moved(m[n].y, mx[n].y, f.y);
             l[n] = fmul2(l[n], f);
             zacc[n] = fmul2(zacc[n], f);
-            off[n] = fmul2(off[n], make_float2(f.x * fo, f.y * fo));
+            if constexpr (F == HS_KV_INT4) off[n] = fmul2(off[n], make_float2(f.x * fo, f.y * fo));
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -719,8 +720,9 @@ struct QAttend {
     // would carry the codes' mean, up to many times what is left of it once the zero points
     // are in, and lose a little of it each time (131072 keys of equal weight, 886 sums a warp:
     // outputs 3.1% of their RMS too low).  So every kRecentre steps each head's mean over
-    // the lane's dimensions moves into an fp32 sum of its own.
-    static constexpr int kRecentre = 8;
+    // the lane's dimensions moves into an fp32 sum of its own (0.2%, the outputs' rounding,
+    // at 8, 16 and 32 steps, which cost 21, 16 and 13 of 536 us).
+    static constexpr int kRecentre = 16;
     __device__ __forceinline__ void recentre() {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {

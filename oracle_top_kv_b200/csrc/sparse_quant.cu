@@ -18,9 +18,9 @@ constexpr int kRowWarps = 1;   // of a prefill CTA: the warps work alone
 constexpr int kStages = 2;
 // 16 heads: Q in shared memory leaves registers for 12 warps on an SM in place of 8 (4-bit,
 // 2048 rows x 4 groups x 1024 keys: 388 us against 483 with Q in registers, when this was
-// chosen; 308 us now).  32 keys a step, of 128-byte rows too, where the work of a step that is
+// chosen; 320 us now).  32 keys a step, of 128-byte rows too, where the work of a step that is
 // not its keys' would weigh twice (8-bit, 1000 rows x 8 groups of 4 heads x 16 blocks of 64:
-// 297 us with 16 keys a step, 222 with 32: 9.8 TB/s of rows, most of which come from L2).
+// 297 us with 16 keys a step, 222 to 228 with 32: 9.5 TB/s of rows, most of them from L2).
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2, 32>;
 template <int D, int F, int NH>
 constexpr size_t kWarpBytes =  // a warp's ring and query
