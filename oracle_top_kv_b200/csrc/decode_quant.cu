@@ -60,14 +60,15 @@ struct Ws {
     float* part;      // [kMaxCtas + units][32 + 16 D]
     float* tmax;      // [units][tiles][16]: largest logit per head, log2 domain
     uint32_t* bits;   // [units][tiles + kBitsPad]: bounds, where a CTA's exceed kBoundCap
-    int tiles;        // of t_kv, at the smallest step
+    int tiles;        // of a unit: t_kv in whole steps, whose tiles are all written
     size_t bytes;
 };
+constexpr int kMaxStep = 32;  // keys of the widest step
 
 static Ws ws_layout(const KParams& p, void* base) {
     Ws w;
     const size_t units = (size_t)p.batch * p.hkv;
-    w.tiles = (p.t_kv + 15) / 16;
+    w.tiles = ((p.t_kv - 1) / kMaxStep + 1) * (kMaxStep / kSub);
     char* c = static_cast<char*>(base);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -114,6 +115,7 @@ __device__ __forceinline__ int share_of(long long x, int G, long long total) {
 
 // Reduces the maxima of a step's 16-key groups over the keys and stores them: a lane has
 // V of them (group, head), and each halving of the lanes of equal t drops half of those.
+// Every group of a step is stored, those past the last key too (-inf).
 struct TileMaxima {
     float* at;  // this unit's [tiles][16]
     template <int NG, int NH>
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<NH>)
                              const int32_t* __restrict__ seq_len, Ws ws) {
     using A = Attend<D, F, NH>;
     constexpr int NK = A::NK;
+    static_assert(kMaxStep % NK == 0, "a unit's tiles hold whole steps");
     extern __shared__ __align__(16) unsigned char smem_raw[];  // rings, reused for partials
     constexpr int kStride = A::Ring::kBytes / 4;
     static_assert(kStride >= A::kPart, "a partial fits a ring");
