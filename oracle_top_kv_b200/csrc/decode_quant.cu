@@ -770,7 +770,10 @@ __global__ void __launch_bounds__(kSelThreads, 1)
             if (srow) srow[x] = exp2f(order_float((uint32_t)tmp[x]));
         }
     }
-    for (int x = tid; x < L - lo; x += blockDim.x) irow[n_best + x] = lo + x;
+    for (int x = tid; x < L - lo; x += blockDim.x) {
+        irow[n_best + x] = lo + x;
+        if (srow) srow[n_best + x] = 0.f;  // keys on bad pages get no score below
+    }
     const int n_out = n_best + L - lo;
     for (int x = n_out + tid; x < p.ksel; x += blockDim.x) {
         irow[x] = -1;
