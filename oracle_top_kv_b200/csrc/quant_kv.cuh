@@ -24,7 +24,8 @@
 //  - p_i s_i is taken relative to 2^10 at the running maximum (growing to
 //    2^14 before O is rescaled) and to a power of two above the largest |s_i|
 //    seen, and rounded to fp16: relative 2^-12 for weights down to 2^-24 of the
-//    largest, an absolute 2^-35 of it below.
+//    largest, an absolute 2^-35 of it below (and in 4 bits the zero points are
+//    weighted by the rounded numbers too, QAttend::centre).
 // Everything else is fp32.  What bounds the kernels is the issue rate: mma.sync
 // holds its scheduler for 8 cycles (measured alone 8.7 cycles, with 4 FFMAs beside it
 // 12.8, with 8 of them 17), so 16 keys of 128 dims and 16 heads take 272 issue cycles
@@ -585,7 +586,7 @@ struct QAttend {
     // + 2 t, + 1
     float o[D / 16][NH][4];
     float2 m[NH];             // p = 2^(logit - m); m lies 10..14 below the running maximum
-    float2 l[NH], zacc[NH];   // sums of p and p z over the lane's keys
+    float2 l[NH], zacc[NH];   // sums over the lane's keys: p, and p z with what step() moves there
     float2 off[NH];           // what recentre() took from the lane's part of O
     float up;                 // power of two above every |scale| seen: O counts in it
 
@@ -644,6 +645,29 @@ struct QAttend {
         }
     }
 
+    // 4-bit codes and zero points are large beside the values that they cancel to, so both
+    // have to be weighted alike: the rounding of p s to fp16, the same for every key of one
+    // weight and scale, would otherwise leave an offset in all dimensions (keys of equal weight
+    // below a larger one: 2% of the outputs' RMS at 131072 of them, 5% at 2^20). With
+    // any c0 and r = p s as rounded,
+    //     sum p v^ = sum r (c - c0) + sum p (z + c0 s) + what r's rounding does to c - c0,
+    // of which the last is the rounding of a weight, 2^-12 of it, where c0 is the code that
+    // stands for 0.  (A c0 of 7.5 for all rows left 0.15% at 131072 one-sided values of mean 0,
+    // this one 0.04%.  The sum of r c0 costs two conversions and an FMA per pair of weights:
+    // 32 sequences of 131072 keys, 16 heads, 552 -> 569 us; 2048-row token layer 320 -> 334.)
+    //
+    // c0 for the lane's keys together: held to the codes' range (no number: 0), so that no
+    // scale makes it large.
+    __device__ static __forceinline__ float centre(const uint32_t (&ent)[NG][2]) {
+        float s = 0.f, z = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            s += entry_scale(ent[i][0]) + entry_scale(ent[i][1]);
+            z += entry_zero(ent[i][0]) + entry_zero(ent[i][1]);
+        }
+        return fminf(fmaxf(__fdividef(-z, s), 0.f), 15.f);
+    }
+
     // One stage's keys.  maxima(step, .): of each 16-key group the largest logits (log2
     // domain) of the lane's two keys, heads 8 n + 2 t, + 1.
     template <class Maxima>
@@ -675,6 +699,8 @@ struct QAttend {
         maxima(at, gm);
         if (__any_sync(0xffffffffu, grow)) rescale(mx, big);
         const float down = up == 0.f ? 0.f : __uint_as_float(0x7f000000u - __float_as_uint(up));
+        const float c0 = F == HS_KV_INT4 ? centre(ent) : 0.f;
+        const float2 take = both(-c0 * up);
         float2 nm[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n)
@@ -685,8 +711,11 @@ struct QAttend {
             uint32_t b[NH][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float2 z = both(entry_zero(ent[i][k]));
-                const float2 sd = both(entry_scale(ent[i][k]) * down);
+                const float s = entry_scale(ent[i][k]);
+                float zero = entry_zero(ent[i][k]);
+                if constexpr (F == HS_KV_INT4) zero = fmaf(c0, s, zero);
+                const float2 z = both(zero);
+                const float2 sd = both(s * down);
 #pragma unroll
                 for (int n = 0; n < NH; ++n) {
                     const float2 y = tc::ffma2(x[i][k][n], q.kf[n], nm[n]);
@@ -694,7 +723,10 @@ struct QAttend {
                     l[n] = tc::fadd2(l[n], p);
                     zacc[n] = tc::ffma2(p, z, zacc[n]);
                     const float2 w = fmul2(p, sd);
-                    b[n][k] = transpose8(pack_f16(w.x, w.y));
+                    const __half2 r = __floats2half2_rn(w.x, w.y);
+                    if constexpr (F == HS_KV_INT4)
+                        zacc[n] = tc::ffma2(__half22float2(r), take, zacc[n]);
+                    b[n][k] = transpose8(*reinterpret_cast<const uint32_t*>(&r));
                 }
             }
             uint32_t v[4][Ring::R::kVW];
