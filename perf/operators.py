@@ -436,7 +436,7 @@ def exact(case, seed):
                 keep = keep[:, :, None].expand(-1, -1, block).reshape(t_q, -1) & (ids <= last[:, None])
             for t in range(0, t_q, 256):
                 part = slice(t, min(t_q, t + 256))
-                k, v = rows_at(torch.where(keep[part], ids[part], 0))
+                k, v = rows_at(ids[part].clamp(min=0))
                 a = torch.einsum("htd,tnd->htn", s["q"][b, heads, part].double(), k) * d ** -0.5
                 a = a.masked_fill(~keep[part][None], -math.inf)
                 l = torch.logsumexp(a, -1)
