@@ -69,8 +69,8 @@ class hs_kv_quant(ctypes.Structure):
 
 def make_kv_quant(fmt, k_codes, k_scale, v_codes, v_scale) -> hs_kv_quant:
     """hs_kv_quant over uint8 code and bf16 {scale, zero} tensors; fmt "int4" or "fp8"."""
-    return hs_kv_quant({"int4": HS_KV_INT4, "fp8": HS_KV_FP8}[fmt], _ptr_here(k_codes), _ptr_here(k_scale),
-                       _ptr_here(v_codes), _ptr_here(v_scale))
+    return hs_kv_quant({"int4": HS_KV_INT4, "fp8": HS_KV_FP8}[fmt],
+                       *_here(k_codes, k_scale, v_codes, v_scale))
 
 
 def make_params(batch, hq, hkv, head_dim, t_q, t_kv, q_offset=0, dtype="bf16", mode="block",
@@ -124,17 +124,13 @@ def load(path: str = LIB_PATH):
     return lib
 
 
-def _current_device():
-    # what torch.cuda.current_device() calls, where this torch has it
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return get() if get else torch.cuda.current_device()
-
-
-def _current_stream(device):
-    # the handle of torch.cuda.current_stream(), without the objects that it makes (a
-    # microsecond per call of this module)
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get else torch.cuda.current_stream(device).cuda_stream
+# The calls behind torch.cuda.current_device() and current_stream(), without the objects
+# that those make (a microsecond or more per call of this module); the public ones where a
+# build of torch has no such names.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (
+    lambda: torch.cuda.current_device())
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _ptr(t):
@@ -147,13 +143,23 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _ptr_here(t):
-    """_ptr of a tensor that has to be on the current device (the quantised cache's entry points)."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.is_cuda and t.get_device() != _current_device():
-        raise ValueError("expected a tensor on the current CUDA device")
-    return _ptr(t)
+def _here(*tensors):
+    """_ptr of each; tensors have to be on the current device (the quantised cache's entry points)."""
+    device, out = None, []
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            at = t.get_device()
+            if at != device:  # the first tensor, or a wrong one
+                if not t.is_cuda:
+                    raise ValueError("expected a CUDA tensor")
+                if device is not None or at != _current_device():
+                    raise ValueError("expected a tensor on the current CUDA device")
+                device = at
+            if not t.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+            t = t.data_ptr()
+        out.append(t)
+    return out
 
 
 def _stream(stream):
@@ -252,33 +258,29 @@ def _ref(struct):
 
 def hs_kv_quant_write(p, kv, pages, k, v, seq_len=None, n_new=None, stream=None):
     """Quantise new rows k, v into the cache (include/hs.h); pages None: contiguous."""
-    _check(load().hs_kv_quant_write(_ref(p), _ref(kv), _ref(pages), _ptr_here(k), _ptr_here(v),
-                                    _ptr_here(seq_len), _ptr_here(n_new), _stream(stream)),
-           "hs_kv_quant_write")
+    _check(load().hs_kv_quant_write(_ref(p), _ref(kv), _ref(pages), *_here(k, v, seq_len, n_new),
+                                    _stream(stream)), "hs_kv_quant_write")
 
 
 def hs_kv_quant_read(p, kv, pages, k, v, seq_len=None, n_new=None, stream=None):
     """Read the rows that hs_kv_quant_write writes with these arguments back into k, v."""
-    _check(load().hs_kv_quant_read(_ref(p), _ref(kv), _ref(pages), _ptr_here(k), _ptr_here(v),
-                                   _ptr_here(seq_len), _ptr_here(n_new), _stream(stream)),
-           "hs_kv_quant_read")
+    _check(load().hs_kv_quant_read(_ref(p), _ref(kv), _ref(pages), *_here(k, v, seq_len, n_new),
+                                   _stream(stream)), "hs_kv_quant_read")
 
 
 def hs_sparse_attn_reuse_quant(p, kv, pages, q_sparse, idx, idx_count, o_global, lse_global,
                                stream=None):
-    _check(load().hs_sparse_attn_reuse_quant(_ref(p), _ref(kv), _ref(pages), _ptr_here(q_sparse),
-                                             _ptr_here(idx), _ptr_here(idx_count), _ptr_here(o_global),
-                                             _ptr_here(lse_global), _stream(stream)),
-           "hs_sparse_attn_reuse_quant")
+    _check(load().hs_sparse_attn_reuse_quant(_ref(p), _ref(kv), _ref(pages),
+                                             *_here(q_sparse, idx, idx_count, o_global, lse_global),
+                                             _stream(stream)), "hs_sparse_attn_reuse_quant")
 
 
 def hs_decode_step_quant(p, kv, pages, kind, q, seq_len, idx, idx_count, o, lse=None,
                          sel_scores=None, workspace=None, stream=None):
     wp, wb = _ws(workspace)
-    _check(load().hs_decode_step_quant(_ref(p), _ref(kv), _ref(pages), int(kind), _ptr_here(q),
-                                       _ptr_here(seq_len), _ptr_here(idx), _ptr_here(idx_count), _ptr_here(o),
-                                       _ptr_here(lse), _ptr_here(sel_scores), wp, wb, _stream(stream)),
-           "hs_decode_step_quant")
+    _check(load().hs_decode_step_quant(_ref(p), _ref(kv), _ref(pages), int(kind),
+                                       *_here(q, seq_len, idx, idx_count, o, lse, sel_scores), wp,
+                                       wb, _stream(stream)), "hs_decode_step_quant")
 
 
 def hs_workspace_size(p, which) -> int:
