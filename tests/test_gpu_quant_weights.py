@@ -88,3 +88,33 @@ def test_sparse_layers_over_equal_keys(decode, skew):
     want, l = _want(t, q, rows)
     P.check_lse(P.f64(lse)[0, :, 0], P.f64(l), "bf16", "lse")
     P.check_o(P.f64(o)[0, :, 0], P.f64(want), "bf16", "o")
+
+
+def test_zero_points_of_8_bit_rows_over_equal_keys():
+    """e4m3 rows of codes of one sign whose zero points take their mean away: held to what
+    include/hs.h states, 2^-12 of each key's weight on scale c (and as much again for the
+    sums), not to what is left of it."""
+    T = 131072
+    gen = torch.Generator(DEV).manual_seed(303)
+    p = _params(1, HEADS, 1, 128, 1, T, k=64, window=0)
+    t = hs.kv_quant_cache(p, "fp8", DEV)
+    t[2].random_(0x70, 0x7f, generator=gen)  # 128 .. 448
+    t[3][..., 0], t[3][..., 1] = 0.01, -2.5
+    t[1][0, 0, ::32, 1] = 0.25
+    gap = 2.8 + torch.arange(HEADS, device=DEV) / (HEADS - 1)
+    q = (gap * np.log(2) * 128 ** 0.5 / (128 * 0.25)).bfloat16()[None, :, None, None].expand(
+        1, HEADS, 1, 128).contiguous()
+    seq = torch.tensor([T], dtype=torch.int32, device=DEV)
+    idx, cnt, o, lse, _ = _decode_outputs(p)
+    hs.hs_decode_step_quant(p, hs.make_kv_quant("fp8", *t), None, hs.HS_DECODE_FULL_INDEX, q, seq,
+                            idx, cnt, o, lse, None, hs.workspace(p, hs.HS_WS_DECODE_FULL_QUANT))
+    assert hs.hs_device_status() == 0
+    c = t[2][0, 0].view(torch.float8_e4m3fn).double()
+    e = t[3][0, 0].double()
+    a = q[0, :, 0].double().sum(-1, keepdim=True) * t[1][0, 0, :, 1].double() / 128 ** 0.5
+    l = torch.logsumexp(a, -1)
+    P.check_lse(P.f64(lse)[0, :, 0], P.f64(l), "bf16", "lse")
+    w = torch.exp(a - l[:, None])
+    want = w @ (c * e[:, :1] + e[:, 1:])
+    bound = 2.0 ** -11 * (w @ (c * e[:, :1]).abs()) + 2.0 ** -8 * want.abs() + 1e-6
+    assert ((o[0, :, 0].double() - want).abs() <= bound).all()
