@@ -311,7 +311,7 @@ hs_status hs_decode_step_paged(const hs_params* p, const hs_pages* pages, int32_
  * A row whose scale is 0 (constant in 4 bits, zero in 8) has codes 0.  A row
  * with a NaN or an infinity, or whose scale or zero overflows bf16, gets NaN
  * for both and reads back as NaN.  The attention takes any codes and entries
- * whose values (and queries) stay below 2^96 in magnitude; beyond that its fp32
+ * whose values (and queries) stay below 2^90 in magnitude; beyond that its fp32
  * products may overflow, and outputs be infinite or NaN.  A zero point in
  * HS_KV_FP8 is taken too, but not compensated as in HS_KV_INT4: the rounding of
  * a key's weight (2^-12 of it) then counts on scale * c, however much of that

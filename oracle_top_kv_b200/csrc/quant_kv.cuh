@@ -26,11 +26,13 @@
 //    seen, and rounded to fp16: relative 2^-12 for weights down to 2^-24 of the
 //    largest, an absolute 2^-35 of it below (and in 4 bits the zero points are
 //    weighted by the rounded numbers too, QAttend::centre).
-// Everything else is fp32.  What bounds the kernels is the issue rate: mma.sync
-// holds its scheduler for 8 cycles (measured alone 8.7 cycles, with 4 FFMAs beside it
-// 12.8, with 8 of them 17), so 16 keys of 128 dims and 16 heads take 272 issue cycles
-// for their 32 MMAs beside some 320 for unpacking, the softmax, the maxima and the reads
-// (32 sequences of 131072 keys, 16 heads of 128: 553 us, 4.1 TB/s of cache).
+// Everything else is fp32.  The kernels are bound by what a scheduler gets issued, not by
+// memory: 16 keys of 128 dims and 16 heads take 294 instructions, 32 of them MMAs, in some
+// 590 cycles at two warps a scheduler (issue active 50%, top stall a fixed-latency wait,
+// DRAM 49%).  An MMA alone takes 8.7 cycles of its scheduler; each FFMA beside it adds one,
+// up to three LOP3s 0.6 each (a fourth 1.6), so that 278 cycles go to the MMAs and the
+// others overlap them in part; how much is lost to the few warps is not settled.
+// (32 sequences of 131072 keys, 16 heads of 128: 569 us, 4.0 TB/s of cache.)
 //
 // One warp takes 16 keys at a time: they are the rows of S^T = K Q^T, 8 heads at a
 // time its columns, and O^T = V^T P^T has 16 dimensions at a time as rows (P^T's

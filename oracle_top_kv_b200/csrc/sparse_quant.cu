@@ -18,7 +18,7 @@ constexpr int kRowWarps = 1;   // of a prefill CTA: the warps work alone
 constexpr int kStages = 2;
 // 16 heads: Q in shared memory leaves registers for 12 warps on an SM in place of 8 (4-bit,
 // 2048 rows x 4 groups x 1024 keys: 388 us against 483 with Q in registers, when this was
-// chosen; 320 us now).  32 keys a step, of 128-byte rows too, where the work of a step that is
+// chosen; 330 us now).  32 keys a step, of 128-byte rows too, where the work of a step that is
 // not its keys' would weigh twice (8-bit, 1000 rows x 8 groups of 4 heads x 16 blocks of 64:
 // 297 us with 16 keys a step, 222 to 228 with 32: 9.5 TB/s of rows, most of them from L2).
 template <int D, int F, int NH> using Attend = QAttend<D, F, NH, kStages, NH == 2, 32>;
@@ -27,7 +27,9 @@ constexpr size_t kWarpBytes =  // a warp's ring and query
     Attend<D, F, NH>::Ring::kBytes + QQuery<D, F, NH, NH == 2>::kBytes;
 // Warps to an SM that the registers are divided for.  8 heads: 14, between few warps and
 // few registers (1000 rows x 8 groups of 4 heads, 1024 keys, at 12, 14, 16 warps: 8-bit
-// blocks 221, 222, 239 us, 4-bit tokens 231, 213, 219, head_dim 64 163, 148, 149).
+// blocks 221, 222, 239 us, 4-bit tokens 231, 213, 219, head_dim 64 163, 148, 149).  Of 8-bit
+// rows of 128 the rings take 17 KB a warp (21 with 16 heads' queries): shared memory holds
+// 12 warps (10), and the 8-bit figures compare register limits only.
 template <int NH> constexpr int kPerSm = NH == 1 ? 14 : 12;
 
 // Writes a unit's heads from a warp's finished accumulators.
